@@ -1,0 +1,284 @@
+// k_gemm_lora.cu — the shared projection with each request's low-rank adapter:
+// rows [seg[s], seg[s+1]) of A belong to request s, whose adapter a = ids[s] adds
+//   scale[a] (A D_a^T) U_a^T,   D_a [r, K], U_a [N, r],
+// to A W^T + bias before the epilogue.
+//
+// Two kernels.  k_lora_down makes T = scale[a] A D_a^T (fp32 sums, r columns
+// wide) and k_gemm_lora runs the dense GEMM of k_gemm_tc.cu whose K loop goes on, for
+// each request that meets the row tile, over the r columns of T and U_a: the
+// low-rank product lands in the same TMEM accumulator, so the output is written
+// once and no epilogue knows of it.
+//
+// A row tile (128 rows) may hold the ends of several requests.  T is therefore
+// stored in slabs, one per (row tile m, request s) that meet, with the rows of
+// other requests zero: the extra K-blocks of a tile then add up to each row's own
+// adapter.  Requests are in row order, so the meeting pairs (m, s) form a
+// monotone chain and m + s numbers the slabs without a table.
+//
+// T enters the second product in bf16, rounded once when the output has 2 bytes
+// (its own rounding is as large).  For fp32 outputs T is split in two bf16
+// parts, high and remainder, and both are multiplied: 2^-17 of the adapter's share
+// is lost instead of 2^-9.
+#include "wd_internal.cuh"
+
+namespace wd {
+namespace lora {
+
+constexpr int BM = tcg::BM, BK = tcg::BK;
+constexpr int MAX_RANK = 256;
+
+struct Args {
+  const int* seg;       // [n_seg + 1], non-decreasing row offsets
+  const int* ids;       // [n_seg]; outside [0, n_adapters): no adapter
+  const float* scale;   // [n_adapters] or null (1)
+  int n_seg, n_adapters, rank, parts;
+  int M, N, K;
+  int m_tiles;
+  bf16* slabs;          // [m_tiles + n_seg][parts][128][rank]
+  int4* tiles;          // [m_tiles]: first request, one past the last, active ones
+};
+
+// Rows [lo, hi) of request s, kept inside the matrix whatever the offsets say.
+__device__ __forceinline__ int seg_lo(const Args& a, int s) { return min(max(a.seg[s], 0), a.M); }
+__device__ __forceinline__ int seg_hi(const Args& a, int s) { return max(min(a.seg[s + 1], a.M), seg_lo(a, s)); }
+__device__ __forceinline__ bool active(const Args& a, int s, int m0) {
+  const int lo = seg_lo(a, s), hi = seg_hi(a, s);
+  return static_cast<unsigned>(a.ids[s]) < static_cast<unsigned>(a.n_adapters) && max(lo, m0) < min(hi, m0 + BM);
+}
+
+// The extra K-blocks of gemm_body: request after request, part after part.
+struct Extra {
+  static constexpr bool ON = true;
+  const Args& a;
+  const CUtensorMap* tmT;   // slabs [rows, rank], box 64 x 128
+  const CUtensorMap* tmU;   // U [n_adapters * N, rank], box 64 x BN
+  struct Row { int first, last, act; };
+  __device__ __forceinline__ Row row(int m) const {
+    const int4 t = a.tiles[m];
+    return {t.x, t.y, t.z};
+  }
+  __device__ __forceinline__ int count(const Row& r) const { return r.act * a.parts * ((a.rank + BK - 1) / BK); }
+  template <typename F>
+  __device__ __forceinline__ void each(const Row& r, int m, int n0, F&& load) const {
+    for (int s = r.first, left = r.act; s < r.last && left > 0; ++s) {
+      if (!active(a, s, m * BM)) continue;
+      --left;
+      for (int p = 0; p < a.parts; ++p)
+        for (int k = 0; k < a.rank; k += BK)
+          if (!load(tmT, k, ((m + s) * a.parts + p) * BM, tmU, k, a.ids[s] * a.N + n0)) return;
+    }
+  }
+};
+
+template <int BN, int MODE>
+__global__ void __launch_bounds__(tcg::threads<MODE>(), 1)
+k_gemm_lora(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmT,
+            const __grid_constant__ CUtensorMap tmU, const Epi ep, const __grid_constant__ Args a) {
+  tcg::gemm_body<BN, MODE, false>(tmA, tmB, tmX, ep, a.M, a.N, a.K, Extra{a, &tmT, &tmU});
+}
+
+// ------------------------------------------------------------------ T = scale A D^T
+// One block per slab: 128 rows x rank, K in 64-wide TMA stages, tcgen05 MMAs of
+// 128 x RN x 16 (RN = rank rounded up to 16; the rows of D behind rank belong to the
+// next adapter and their columns are not stored).  Warp 0 loads, warp 1 issues,
+// warps 2-5 take the accumulator out.  Blocks of the first m_tiles also write
+// their row tile's entry of the table.
+constexpr int STAGES = 4, THREADS = 192;
+__host__ __device__ constexpr int stage_bytes(int rn) { return BM * BK * 2 + rn * BK * 2; }
+constexpr int smem_bytes(int rn) { return 1024 + STAGES * stage_bytes(rn) + 256; }
+
+enum : unsigned { SITE_EMPTY = 0x401, SITE_FULL = 0x402, SITE_DONE = 0x403, SITE_DRAIN = 0x404 };
+
+__global__ void __launch_bounds__(THREADS, 1)
+k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmD,
+            const __grid_constant__ Args a, int rn, uint32_t tmem_cols, uint32_t idesc) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[STAGES], empty[STAGES], done;
+  __shared__ uint32_t tmem_slot;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slab = blockIdx.x;
+
+  if (slab < a.m_tiles && threadIdx.x == 0) {
+    // requests [first, last) meet rows [m0, m0 + 128): the first that ends behind m0, up to
+    // the first that starts at or behind the tile's end
+    const int m0 = slab * BM;
+    int lo = 0, hi = a.n_seg;
+    while (lo < hi) { const int mid = (lo + hi) >> 1; if (a.seg[mid + 1] > m0) hi = mid; else lo = mid + 1; }
+    int act = 0, s = lo;
+    for (; s < a.n_seg && a.seg[s] < m0 + BM; ++s) act += active(a, s, m0);
+    a.tiles[slab] = make_int4(lo, s, act, 0);
+  }
+  // the pair (m, s) of this slab: the last s whose request starts before the end of tile slab - s
+  int s = -1;
+  {
+    int lo = 0, hi = a.n_seg;   // first s that does not
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (a.seg[mid] < (slab - mid + 1) * BM) lo = mid + 1; else hi = mid;
+    }
+    s = lo - 1;
+  }
+  const int m = slab - s, m0 = m * BM;
+  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, s, m0)) return;   // no such pair: the whole block leaves
+  const int ad = a.ids[s];
+  const int k_iters = (a.K + BK - 1) / BK;
+  const int sb = stage_bytes(rn);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    mbar_init(&done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) { tmem_alloc(&tmem_slot, tmem_cols); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t issued = 0, last_par = 0;
+      for (int k = 0; k < k_iters; ++k) {
+        const int st = k % STAGES;
+        const uint32_t ph = (k / STAGES) & 1u;
+        if (!mbar_wait(&empty[st], ph ^ 1u, SITE_EMPTY)) break;
+        mbar_arrive_expect_tx(&full[st], sb);
+        tma_load_2d(smem + st * sb, &tmA, k * BK, m0, &full[st]);
+        tma_load_2d(smem + st * sb + BM * BK * 2, &tmD, k * BK, ad * a.rank, &full[st]);
+        issued |= 1u << st;
+        last_par = (last_par & ~(1u << st)) | (ph << st);
+      }
+      for (int i = 0; i < STAGES; ++i)
+        if (issued & (1u << i)) mbar_wait(&full[i], (last_par >> i) & 1u, SITE_DRAIN);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t base = smem_u32(smem);
+      for (int k = 0; k < k_iters; ++k) {
+        const int st = k % STAGES;
+        if (!mbar_wait(&full[st], (k / STAGES) & 1u, SITE_FULL)) break;
+        tc_fence_after();
+        const uint64_t da = sdesc_sw128(base + st * sb, 16, 1024);
+        const uint64_t db = sdesc_sw128(base + st * sb + BM * BK * 2, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk) umma_ss(tmem, da + kk * 2, db + kk * 2, idesc, (k | kk) != 0);
+        umma_commit(&empty[st]);
+      }
+      umma_commit(&done);
+      mbar_wait(&done, 0, SITE_DRAIN);
+    }
+    __syncwarp();
+  } else if (mbar_wait_warp(&done, 0, SITE_DONE)) {
+    tc_fence_after();
+    const int q = warp & 3, r = q * 32 + lane, row = m0 + r;
+    const bool mine = row >= seg_lo(a, s) && row < seg_hi(a, s);
+    const float sc = a.scale ? a.scale[ad] : 1.f;
+    bf16* hi = a.slabs + (static_cast<int64_t>(slab) * a.parts * BM + r) * a.rank;
+    bf16* rem = hi + static_cast<int64_t>(BM) * a.rank;
+    for (int c = 0; c < a.rank; c += 32) {
+      uint32_t u[32];
+      tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, u);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (c + 8 * j >= a.rank) continue;
+        uint32_t w[4], x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v0 = mine ? sc * __uint_as_float(u[8 * j + 2 * i]) : 0.f;
+          const float v1 = mine ? sc * __uint_as_float(u[8 * j + 2 * i + 1]) : 0.f;
+          w[i] = pack_bf16x2(v0, v1);
+          const float2 f = unpack_bf16x2(w[i]);
+          x[i] = pack_bf16x2(v0 - f.x, v1 - f.y);
+        }
+        *reinterpret_cast<uint4*>(hi + c + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (a.parts == 2) *reinterpret_cast<uint4*>(rem + c + 8 * j) = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, tmem_cols);
+}
+
+}  // namespace lora
+
+// ------------------------------------------------------------------ host side
+static size_t lora_slab_bytes(int64_t slabs, int rank) { return static_cast<size_t>(slabs) * 2 * lora::BM * rank * 2; }
+
+size_t gemm_lora_bytes(int M, int n_seg, int rank) {
+  const int64_t mt = (static_cast<int64_t>(M) + lora::BM - 1) / lora::BM;
+  return ((lora_slab_bytes(mt + n_seg, rank) + 255) & ~size_t(255)) + static_cast<size_t>(mt) * sizeof(int4);
+}
+
+template <int BN, int MODE>
+static wd_status launch_lora(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tt, const CUtensorMap& tu,
+                             const Epi& ep, const lora::Args& a, cudaStream_t st) {
+  using C = tcg::Cfg<BN>;
+  WD_TRY((allow_smem<lora::k_gemm_lora<BN, MODE>>(C::smem(MODE))));
+  const int tiles = a.m_tiles * (a.N / BN);
+  const int grid = tiles < sm_count() ? tiles : sm_count();
+  CUtensorMap tx = ta;
+  if (MODE == EPI_RESID) WD_TRY(make_tmap_f32(&tx, ep.out, a.M, a.N, ep.ldo, 32, 32));
+  if (tcg::staged2<MODE>() && (BN / tcg::epi_wg<MODE>()) % 64 == 0)
+    WD_TRY(make_tmap_2b(&tx, ep.out, a.M, a.N, ep.ldo, MODE == EPI_STORE_F16));
+  Trace tr(KC_GEMM, st);
+  lora::k_gemm_lora<BN, MODE><<<grid, tcg::threads<MODE>(), C::smem(MODE), st>>>(ta, tb, tx, tt, tu, ep, a);
+  return launch_status("gemm_lora");
+}
+
+template <int BN>
+static wd_status dispatch_lora(int mode, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tt,
+                               const CUtensorMap& tu, const Epi& ep, const lora::Args& a, cudaStream_t st) {
+  switch (mode) {
+    case EPI_STORE: return launch_lora<BN, EPI_STORE>(ta, tb, tt, tu, ep, a, st);
+    case EPI_GELU: return launch_lora<BN, EPI_GELU>(ta, tb, tt, tu, ep, a, st);
+    case EPI_F32: return launch_lora<BN, EPI_F32>(ta, tb, tt, tu, ep, a, st);
+    case EPI_RESID: return launch_lora<BN, EPI_RESID>(ta, tb, tt, tu, ep, a, st);
+    case EPI_STORE_F16: return launch_lora<BN, EPI_STORE_F16>(ta, tb, tt, tu, ep, a, st);
+  }
+  set_error("gemm_lora: bad epilogue %d", mode);
+  return WD_ERR_ARG;
+}
+
+static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, const wd_lora& l, int mode, const Epi& ep,
+                           void* ws, cudaStream_t st) {
+  lora::Args a{};
+  a.seg = l.seg; a.ids = l.adapter; a.scale = l.scale;
+  a.n_seg = l.n_seg; a.n_adapters = l.n_adapters; a.rank = l.rank;
+  a.parts = (mode == EPI_F32 || mode == EPI_RESID) ? 2 : 1;
+  a.M = M; a.N = N; a.K = K;
+  a.m_tiles = (M + lora::BM - 1) / lora::BM;
+  const int64_t slabs = static_cast<int64_t>(a.m_tiles) + l.n_seg;
+  a.slabs = static_cast<bf16*>(ws);
+  a.tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + ((lora_slab_bytes(slabs, l.rank) + 255) & ~size_t(255)));
+  const int rn = (l.rank + 15) / 16 * 16;
+  CUtensorMap ta, tb, td, tt, tu;
+  WD_TRY(make_tmap_bf16(&ta, A, M, K, K, lora::BK, lora::BM));
+  WD_TRY(make_tmap_bf16(&td, l.down, static_cast<int64_t>(l.n_adapters) * l.rank, K, K, lora::BK, rn));
+  uint32_t cols = 32;
+  while (cols < static_cast<uint32_t>(rn)) cols *= 2;
+  WD_TRY((allow_smem<lora::k_lora_down>(lora::smem_bytes(lora::MAX_RANK))));
+  {
+    Trace tr(KC_GEMM, st);
+    lora::k_lora_down<<<static_cast<unsigned>(slabs), lora::THREADS, lora::smem_bytes(rn), st>>>(
+        ta, td, a, rn, cols, idesc_bf16(lora::BM, rn, 0, 0));
+  }
+  WD_TRY(launch_status("lora_down"));
+  const int BN = (N % 256 == 0) ? 256 : ((N % 128 == 0) ? 128 : 64);
+  WD_TRY(make_tmap_bf16(&tb, W, N, K, K, lora::BK, BN));
+  WD_TRY(make_tmap_bf16(&tt, a.slabs, slabs * a.parts * lora::BM, l.rank, l.rank, lora::BK, lora::BM));
+  WD_TRY(make_tmap_bf16(&tu, l.up, static_cast<int64_t>(l.n_adapters) * N, l.rank, l.rank, lora::BK, BN));
+  switch (BN) {
+    case 256: return dispatch_lora<256>(mode, ta, tb, tt, tu, ep, a, st);
+    case 128: return dispatch_lora<128>(mode, ta, tb, tt, tu, ep, a, st);
+    default: return dispatch_lora<64>(mode, ta, tb, tt, tu, ep, a, st);
+  }
+}
+
+}  // namespace wd

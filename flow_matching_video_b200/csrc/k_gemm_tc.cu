@@ -142,10 +142,19 @@ __device__ __forceinline__ void epilogue32(const Epi& ep, int64_t m, int n, cons
 }
 
 // ------------------------------------------------------------------ kernel
-template <int BN, int MODE, bool F8>
-__global__ void __launch_bounds__(threads<MODE>(), 1)
-k_gemm_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-          const __grid_constant__ CUtensorMap tmX, const Epi ep, int M, int N, int K) {
+// Further K-blocks of a row tile, accumulated after the K loop of A and B: none
+// for the plain GEMM; the low-rank products of k_gemm_lora.cu implement these.
+struct NoExtra {
+  static constexpr bool ON = false;
+  struct Row {};
+  __device__ __forceinline__ Row row(int) const { return {}; }
+  __device__ __forceinline__ int count(const Row&) const { return 0; }
+  template <typename F> __device__ __forceinline__ void each(const Row&, int, int, F&&) const {}
+};
+
+template <int BN, int MODE, bool F8, typename X>
+__device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmX,
+                                          const Epi& ep, int M, int N, int K, const X& ex) {
   using C = Cfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -198,6 +207,19 @@ k_gemm_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
+        if constexpr (X::ON) {
+          if (ok) ex.each(ex.row(t / n_tiles), t / n_tiles, n0, [&](const CUtensorMap* ta, int ac, int ar,
+                                                                    const CUtensorMap* tb, int bc, int br) -> bool {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, SITE_EMPTY)) return ok = false;
+            mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+            tma_load_2d(sA + stage * C::A_BYTES, ta, ac, ar, &full[stage]);
+            tma_load_2d(sB + stage * C::B_BYTES, tb, bc, br, &full[stage]);
+            issued |= 1u << stage;
+            last_par = (last_par & ~(1u << stage)) | (phase << stage);
+            if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+            return true;
+          });
+        }
       }
       // Let every copy this thread issued land before the CTA can exit.
       for (int s = 0; s < C::STAGES; ++s)
@@ -219,7 +241,9 @@ k_gemm_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, SITE_TEMPTY)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
-        for (int k = 0; k < k_iters; ++k) {
+        int iters = k_iters;
+        if constexpr (X::ON) iters += ex.count(ex.row(t / n_tiles));
+        for (int k = 0; k < iters; ++k) {
           if (!mbar_wait(&full[stage], phase, SITE_FULL)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_lo = a_lo0 + stage * (C::A_BYTES >> 4), b_lo = b_lo0 + stage * (C::B_BYTES >> 4);
@@ -353,6 +377,13 @@ k_gemm_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUten
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+template <int BN, int MODE, bool F8>
+__global__ void __launch_bounds__(threads<MODE>(), 1)
+k_gemm_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+          const __grid_constant__ CUtensorMap tmX, const Epi ep, int M, int N, int K) {
+  gemm_body<BN, MODE, F8>(tmA, tmB, tmX, ep, M, N, K, NoExtra{});
 }
 
 }  // namespace tcg

@@ -1,0 +1,392 @@
+// k_rows_packed.cu — the row-wise operators of packed batches: QK-RMSNorm with
+// rotary positions of several axes per token, and the residual addition with
+// the norm behind it (output in fp32, bf16, or e4m3 with one scale per row).
+// Both read every element once and hold the row in registers; both are bound
+// by HBM.
+#include "wd_internal.cuh"
+
+#include <cuda_fp8.h>
+
+#include <cmath>
+
+namespace wd {
+namespace rows {
+
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int NV = 8;   // 8-element chunks that a lane holds of its row, at most
+
+// Eight consecutive elements of type T as fp32 (16-byte accesses; the cache
+// hint is "streaming": nothing here is read twice).
+template <typename T> struct Chunk;
+template <> struct Chunk<float> {
+  uint4 u[2];
+  __device__ __forceinline__ void load(const float* p) {
+    u[0] = __ldcs(reinterpret_cast<const uint4*>(p));
+    u[1] = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+  }
+  __device__ static __forceinline__ void store(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+template <> struct Chunk<bf16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const bf16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack_bf16x2(w[i]);
+      v[2 * i] = f.x; v[2 * i + 1] = f.y;
+    }
+  }
+  __device__ static __forceinline__ void store(bf16* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+};
+template <> struct Chunk<f16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const f16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x; v[2 * i + 1] = f.y;
+    }
+  }
+  __device__ static __forceinline__ void store(f16* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+                                              pack_f16x2(v[6], v[7]));
+  }
+};
+
+__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// Sum (or maximum) of one value per lane over the WPR warps of a row; `red` has one
+// float per warp and is reused: a second reduction of the same loop pass needs another one.
+template <int WPR, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* red, int warp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, w) : v + w;
+  }
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    v = red[warp / WPR * WPR];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) v = MAX ? fmaxf(v, red[warp / WPR * WPR + i]) : v + red[warp / WPR * WPR + i];
+  }
+  return v;
+}
+
+// ============================================================ QK-RMSNorm + rotary positions of three axes
+// For each token and head, pair p of the head's channels (2p, 2p+1) = (re, im)
+// turns by pos[axis(p)] * step[axis] * theta^(-2 p_s / d_s), with p_s counted
+// inside the axis's section of d_s channels; before that, with gains, the row
+// (all heads) is RMS-normalised.
+//
+// Angles: one position's share of a turn, f = step * theta^(-2 p_s / d_s) / 2 pi
+// mod 1, is held as a 64-bit fraction (made on the host in extended precision).
+// pos * f mod 2^64 is then the angle in 2^-64 turns, exact but for f's own
+// rounding (|pos| 2^-65 turns), so far positions lose nothing; the quadrant is
+// its two leading bits and only the rest goes to sincospif.
+constexpr int MAX_PAIRS = 128;   // head width up to 256
+struct RopeArgs {
+  const int* pos;                     // [rows, 3]
+  const void* in[2];
+  void* out[2];
+  const float* gain[2];
+  int64_t in_rs[2], out_rs[2];
+  int D[2];                           // heads * dh of each tensor
+  int tensors;                        // 1: q only, 2: q and k
+  int64_t rows;
+  int dh, p1, p2;                     // pairs [0, p1) frame, [p1, p2) row, [p2, dh / 2) column
+  float eps;
+  uint64_t freq[MAX_PAIRS];
+};
+
+__device__ __forceinline__ float2 turn(int pos, uint64_t f) {
+  const uint32_t u = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<int64_t>(pos)) * f) >> 32);
+  const uint32_t quad = (u + 0x20000000u) >> 30;                       // nearest quarter turn
+  const int rest = static_cast<int>(u - (quad << 30));                 // within an eighth of a turn of it
+  float s, c;
+  sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s, &c);   // rest * 2^-31 half turns
+  const float a = (quad & 1u) ? -s : c, b = (quad & 1u) ? c : s;
+  return (quad & 2u) ? make_float2(-a, -b) : make_float2(a, b);
+}
+
+// WPR warps hold one row of one tensor; a block of 8 warps takes 8 / (WPR *
+// tensors) tokens at a time, whose cosines and sines all its warps share in
+// shared memory: dh / 2 of them a token against heads * dh / 2 rotations each
+// in q and k.  The row's loads are issued before the angles are computed.
+template <typename T, int WPR>
+__global__ void __launch_bounds__(THREADS) k_qknorm_rope_axes(const __grid_constant__ RopeArgs a) {
+  __shared__ uint64_t freq[MAX_PAIRS];
+  __shared__ __align__(16) float2 cs[2][WARPS / WPR][MAX_PAIRS];
+  __shared__ float red[2][WARPS];
+  const int half = a.dh >> 1;
+  for (int i = threadIdx.x; i < half; i += THREADS) freq[i] = a.freq[i];
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = warp / WPR, in_row = (warp % WPR) * 32 + lane;
+  const int tokens = WARPS / WPR / a.tensors;            // of one pass of the block
+  const int which = a.tensors == 2 ? unit & 1 : 0, mine = a.tensors == 2 ? unit >> 1 : unit;
+  const int D = a.D[which];
+  const float* gain = a.gain[which];
+  int buf = 0;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens; row0 < a.rows;
+       row0 += static_cast<int64_t>(gridDim.x) * tokens, buf ^= 1) {
+    const int64_t row = row0 + mine;
+    const bool live = row < a.rows;
+    const T* x = static_cast<const T*>(a.in[which]) + row * a.in_rs[which];
+    Chunk<T> ch[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * WPR * 32 + in_row) * 8;
+      if (live && c < D) ch[i].load(x + c);
+    }
+    for (int i = threadIdx.x; i < tokens * half; i += THREADS) {
+      const int tk = i / half, p = i - tk * half;
+      if (row0 + tk < a.rows)
+        cs[buf][tk][p] = turn(a.pos[(row0 + tk) * 3 + (p < a.p1 ? 0 : (p < a.p2 ? 1 : 2))], freq[p]);
+    }
+    float r = 1.f;
+    if (gain) {   // the same for a whole tensor; with WPR > 1 a unit's warps agree, the others wait below
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * WPR * 32 + in_row) * 8;
+        if (live && c < D) {
+          float v[8];
+          ch[i].get(v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) ss += v[k] * v[k];
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      r = ss;
+      if (WPR > 1 && lane == 0) red[buf][warp] = ss;
+    }
+    __syncthreads();   // the angles (and the warps' sums); the other buffers serve the next pass
+    if (!live) continue;
+    if (gain) {
+      if constexpr (WPR > 1) {
+        r = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) r += red[buf][unit * WPR + i];
+      }
+      r = rsqrtf(r / D + a.eps);
+    }
+    T* y = static_cast<T*>(a.out[which]) + row * a.out_rs[which];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * WPR * 32 + in_row) * 8;
+      if (c >= D) break;
+      float v[8];
+      ch[i].get(v);
+      if (gain) {
+        float g[8];
+        load8f(gain + c, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = v[k] * r * g[k];
+      }
+      const float4* t4 = reinterpret_cast<const float4*>(&cs[buf][mine][(c % a.dh) >> 1]);
+      const float4 ta = t4[0], tb = t4[1];
+      const float co[4] = {ta.x, ta.z, tb.x, tb.z}, si[4] = {ta.y, ta.w, tb.y, tb.w};
+      float o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[2 * k] = v[2 * k] * co[k] - v[2 * k + 1] * si[k];
+        o[2 * k + 1] = v[2 * k] * si[k] + v[2 * k + 1] * co[k];
+      }
+      Chunk<T>::store(y + c, o);
+    }
+  }
+}
+
+// ============================================================ residual addition + norm
+// s = x + y; n = norm(s) * gain + beta per row, with the statistics and n taken
+// from the fp32 sum; s is stored in x's type, n in fp32, bf16 or e4m3 (codes
+// e4m3(n / scale), scale = amax / 448, as k_quant_rows_e4m3).  LayerNorm's
+// variance is summed after the mean is known (the row is in registers), so no
+// difference of large numbers is taken.
+struct AddNormArgs {
+  const void *x, *y;      // y null: no addition
+  const float *gain, *beta;
+  void *sum, *out;        // sum null: not stored
+  float* scale;
+  int64_t rows;
+  int D, rms;
+  float eps;
+};
+
+template <typename TX, typename TY, typename TO, int WPR>
+__global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a) {
+  constexpr bool Q = std::is_same<TO, uint8_t>::value;
+  __shared__ float red[3][WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int in_row = (warp % WPR) * 32 + lane;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (WARPS / WPR) + warp / WPR;
+  const bool live = row < a.rows;   // no early return: the reductions below are the whole block's
+  const int D = a.D;
+  const int64_t base = live ? row * D : 0;
+  float v[NV][8];
+  {
+    Chunk<TX> cx[NV];
+    Chunk<TY> cy[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * WPR * 32 + in_row) * 8;
+      if (live && c < D) cx[i].load(static_cast<const TX*>(a.x) + base + c);
+    }
+    if (a.y) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * WPR * 32 + in_row) * 8;
+        if (live && c < D) cy[i].load(static_cast<const TY*>(a.y) + base + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * WPR * 32 + in_row) * 8;
+      if (live && c < D) {
+        cx[i].get(v[i]);
+        if (a.y) {
+          float w[8];
+          cy[i].get(w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] += w[k];
+        }
+        if (a.sum) Chunk<TX>::store(static_cast<TX*>(a.sum) + base + c, v[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+      }
+    }
+  }
+  float mean = 0.f;
+  if (!a.rms) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[i][k];
+    mean = row_reduce<WPR, false>(s, red[0], warp) / D;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * WPR * 32 + in_row) * 8;
+    if (c < D) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[i][k] -= mean;
+        q += v[i][k] * v[i][k];
+      }
+    }
+  }
+  const float rstd = rsqrtf(row_reduce<WPR, false>(q, red[1], warp) / D + a.eps);
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * WPR * 32 + in_row) * 8;
+    if (c < D) {
+      float g[8];
+      if (a.gain) {
+        load8f(a.gain + c, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * rstd * g[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] *= rstd;
+      }
+      if (a.beta) {
+        load8f(a.beta + c, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] += g[k];
+      }
+      if constexpr (Q) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[i][k]));
+      } else if (live) {
+        Chunk<TO>::store(static_cast<TO*>(a.out) + base + c, v[i]);
+      }
+    }
+  }
+  if constexpr (Q) {
+    amax = row_reduce<WPR, true>(amax, red[2], warp);
+    const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * WPR * 32 + in_row) * 8;
+      if (c < D) {
+        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 8; k += 2)
+          w[k >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+                           make_float2(__fdiv_rn(v[i][k], sc), __fdiv_rn(v[i][k + 1], sc)), __NV_SATFINITE, __NV_E4M3))
+                       << (8 * (k & 3));
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + base + c) = make_uint2(w[0], w[1]);
+      }
+    }
+    if (in_row == 0) a.scale[row] = sc;
+  }
+}
+
+}  // namespace rows
+
+// ------------------------------------------------------------------ host side
+constexpr int ROW_MAX = rows::NV * 8 * 32 * 4;   // 8192: four warps a row
+
+template <typename T>
+static wd_status qknorm_rope_axes(const rows::RopeArgs& a, cudaStream_t st) {
+  const int D = a.tensors == 2 && a.D[1] > a.D[0] ? a.D[1] : a.D[0];
+  const int wpr = D <= rows::NV * 8 * 32 ? 1 : 4;
+  const int tokens = rows::WARPS / wpr / a.tensors;
+  const int64_t want = (a.rows + tokens - 1) / tokens, most = static_cast<int64_t>(sm_count()) * 8;
+  const unsigned grid = static_cast<unsigned>(want < most ? want : most);
+  Trace tr(KC_ROPE, st);
+  if (wpr == 1) rows::k_qknorm_rope_axes<T, 1><<<grid, rows::THREADS, 0, st>>>(a);
+  else rows::k_qknorm_rope_axes<T, 4><<<grid, rows::THREADS, 0, st>>>(a);
+  return launch_status("qknorm_rope_axes");
+}
+
+template <typename TX, typename TY, typename TO>
+static wd_status add_norm_t(const rows::AddNormArgs& a, cudaStream_t st) {
+  const int wpr = a.D <= rows::NV * 8 * 32 ? 1 : 4;
+  const int64_t grid = (a.rows + rows::WARPS / wpr - 1) / (rows::WARPS / wpr);
+  if (grid > 0x7fffffff) { set_error("add_norm: %lld rows", (long long)a.rows); return WD_ERR_SHAPE; }
+  Trace tr(KC_NORM, st);
+  if (wpr == 1) rows::k_add_norm<TX, TY, TO, 1><<<static_cast<unsigned>(grid), rows::THREADS, 0, st>>>(a);
+  else rows::k_add_norm<TX, TY, TO, 4><<<static_cast<unsigned>(grid), rows::THREADS, 0, st>>>(a);
+  return launch_status("add_norm");
+}
+
+template <typename TX, typename TY>
+static wd_status add_norm_o(const rows::AddNormArgs& a, int out_dtype, cudaStream_t st) {
+  if (out_dtype == WD_F32) return add_norm_t<TX, TY, float>(a, st);
+  if (out_dtype == WD_BF16) return add_norm_t<TX, TY, bf16>(a, st);
+  return add_norm_t<TX, TY, uint8_t>(a, st);
+}
+
+static wd_status add_norm(const rows::AddNormArgs& a, int x_dtype, int y_dtype, int out_dtype, cudaStream_t st) {
+  if (x_dtype == WD_F32)
+    return y_dtype == WD_F32 ? add_norm_o<float, float>(a, out_dtype, st) : add_norm_o<float, bf16>(a, out_dtype, st);
+  return y_dtype == WD_F32 ? add_norm_o<bf16, float>(a, out_dtype, st) : add_norm_o<bf16, bf16>(a, out_dtype, st);
+}
+
+}  // namespace wd

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 #include <cstdio>
@@ -28,6 +29,19 @@ void set_error(const char* fmt, ...);
   } while (0)
 
 wd_status launch_status(const char* what);   // cudaGetLastError -> WD_ERR_CUDA + message
+
+// Allows kernel F `bytes` of dynamic shared memory on the current device, once per device.
+template <auto F>
+wd_status allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) { set_error("no CUDA device"); return WD_ERR_CUDA; }
+  if (dev < 64 && done[dev].load(std::memory_order_relaxed)) return WD_OK;
+  const cudaError_t e = cudaFuncSetAttribute(F, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) { set_error("%d bytes of shared memory: %s", bytes, cudaGetErrorString(e)); return WD_ERR_CUDA; }
+  if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return WD_OK;
+}
 
 // ------------------------------------------------------------------ tracing
 // Kernel classes for launch accounting (same order as wd_kernel_class in wd.h).

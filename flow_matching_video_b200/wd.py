@@ -17,7 +17,7 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libwd.so not built ({LIB_PATH}); run `python -m flow_matching_video_b200.build`")
 _lib = C.CDLL(LIB_PATH)
 
-WD_F32, WD_BF16, WD_F16 = 0, 1, 2
+WD_F32, WD_BF16, WD_F16, WD_E4M3 = 0, 1, 2, 3
 WD_NORM_LAYER, WD_NORM_RMS = 0, 1
 EPI_STORE, EPI_GELU, EPI_F32, EPI_RESID, EPI_STORE_F16 = 0, 1, 2, 3, 5
 STATUS = {0: "WD_OK", 1: "WD_ERR_ARG", 2: "WD_ERR_SHAPE", 3: "WD_ERR_DTYPE", 4: "WD_ERR_ALIGN",
@@ -56,6 +56,39 @@ class wd_attn_fp8_layout(C.Structure):
     _fields_ = [(f, C.c_size_t) for f in ("q8", "sq", "k8", "sk", "v8t", "sv", "v_amax", "bytes")] + \
                [("lkp", C.c_int64)]
 
+
+class wd_rope_axes(C.Structure):
+    _fields_ = [("sec", C.c_int * 3), ("theta", C.c_double), ("step", C.c_double * 3)]
+
+    @classmethod
+    def of(cls, sections, theta=10000.0, step=(1.0, 1.0, 1.0)):
+        """sections: a head's channels of (frame, row, column)."""
+        return cls((C.c_int * 3)(*sections), theta, (C.c_double * 3)(*step))
+
+
+class wd_lora(C.Structure):
+    _fields_ = [("n_seg", C.c_int), ("n_adapters", C.c_int), ("rank", C.c_int)] + \
+               [(f, C.c_void_p) for f in ("seg", "adapter", "down", "up", "scale")]
+
+    @classmethod
+    def of(cls, seg, adapter, down, up, scale=None):
+        """Adapters of a packed batch: seg [n_seg + 1] and adapter [n_seg] int32, down
+        [n_adapters, rank, K] and up [n_adapters, N, rank] bf16, scale [n_adapters]
+        fp32 or None; dense tensors of one device, which the struct keeps alive."""
+        na, r, k = _dims(down, 3, "down")
+        n = _dims(up, 3, "up")[1]
+        ns = adapter.numel()
+        _take("wd_lora", seg, "torch.int32", (ns + 1,))
+        _take("wd_lora", adapter, "torch.int32", (ns,))
+        _take("wd_lora", down, "torch.bfloat16", (na, r, k))
+        _take("wd_lora", up, "torch.bfloat16", (na, n, r))
+        if scale is not None:
+            _take("wd_lora", scale, "torch.float32", (na,))
+        out = cls(ns, na, r, _p(seg), _p(adapter), _p(down), _p(up), _p(scale))
+        out.tensors = (seg, adapter, down, up, scale)
+        return out
+
+
 # exported symbol -> (restype, argtypes)
 _P, _I, _F, _S, _L = C.c_void_p, C.c_int, C.c_float, C.c_size_t, C.c_int64
 _PD = C.POINTER(wd_dims)
@@ -91,6 +124,12 @@ SIGNATURES = {
     "wd_attention_fp8": (_I, [_I, _L, _L, _I, _I, _P, _S, _P, _L, _P]),
     "wd_quant_rows_e4m3": (_I, [_I, _I, _I, _P, _P, _P, _P]),
     "wd_gemm_fp8": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P]),
+    "wd_attention_packed": (_I, [_I, _I, _I, _I, _I, _P, _L, _L, _P, _P, _P, _L, _L, _P, _F, _P, _I, _P, _L, _P]),
+    "wd_qknorm_rope_axes": (_I, [_I, _L, _I, C.POINTER(wd_rope_axes), _P, _P, _L, _I, _P, _P, _L, _P, _L, _I, _P, _P, _L,
+                                 _F, _P]),
+    "wd_add_norm": (_I, [_L, _I, _I, _P, _I, _P, _I, _P, _P, _F, _P, _I, _P, _P, _P]),
+    "wd_gemm_lora_bytes": (_S, [_I, _I, _I]),
+    "wd_gemm_lora": (_I, [_I, _I, _I, _P, _P, _P, C.POINTER(wd_lora), _I, _P, _P, _P, _P, _S, _P]),
     "wd_test_exp2": (_I, [_P, _P, _P, _P, _P, _L, _P]),
     "wd_test_gelu": (_I, [_P, _P, _P, _P, _L, _P]),
     "wd_test_wait_timeout": (_I, [C.c_uint64, C.c_uint, _P, _P]),
@@ -125,6 +164,48 @@ def _stream(stream):
 def _ok(status: int, where: str):
     if status != 0:
         raise WDError(status, where)
+
+
+def _dims(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name}: {t.dim()} dimensions, not {n}")
+    return tuple(t.shape)
+
+
+def _take(where, t, dtype, shape):
+    """A dense tensor of this element type (by name) and shape."""
+    if str(t.dtype) != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{where}: a dense {dtype} tensor {list(shape)} is wanted, not {t.dtype} {list(t.shape)}"
+                         f" with strides {list(t.stride())}")
+
+
+def _rows(where, t, dtype, width, rows=None):
+    """Row stride of a 2D tensor [rows, width] whose rows are dense."""
+    if str(t.dtype) != dtype or t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows) or \
+            (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{where}: {dtype} rows of {width} dense elements are wanted, not {t.dtype} {list(t.shape)}"
+                         f" with strides {list(t.stride())}")
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+_TORCH = {WD_F32: "torch.float32", WD_BF16: "torch.bfloat16", WD_F16: "torch.float16", WD_E4M3: "torch.uint8"}
+
+
+def _torch_type(where, dtype):
+    if dtype not in _TORCH:
+        raise ValueError(f"{where}: dtype {dtype}")
+    return _TORCH[dtype]
+
+
+def _launch(where, tensors, stream, call):
+    """call(stream handle) on the tensors' own device: its current stream, or the one given."""
+    import torch
+    live = [t for t in tensors if t is not None]
+    dev = live[0].device
+    if any(t.device != dev for t in live) or dev.type != "cuda":
+        raise ValueError(f"{where}: tensors on {sorted({str(t.device) for t in live})}, one CUDA device is wanted")
+    with torch.cuda.device(dev):
+        _ok(call(_stream(stream)), where)
 
 
 def make_dims(d) -> wd_dims:
@@ -254,6 +335,90 @@ def wd_attention(dtype, batch, Lq, heads, dh, q, k1, v1, n1, kv1_shared, o, k2=N
                  stream=None):
     _ok(_lib.wd_attention(dtype, batch, Lq, heads, dh, _p(q), _p(k1), _p(v1), n1, int(kv1_shared), _p(k2), _p(v2),
                           n2, int(kv2_shared), _p(o), _stream(stream)), "wd_attention")
+
+
+# Packed batches.  Sizes and strides come from the tensors, which are checked against
+# them; the launch goes to the tensors' device.
+def wd_attention_packed(dtype, heads, kv_heads, dh, q, k, v, cu_q, cu_k, scale, o, bias=None, stream=None):
+    """q, o [q_rows, heads*dh], k, v [k_rows, kv_heads*dh] (row strides may differ, k and v
+    share theirs), cu_q, cu_k int32 [n_seq + 1], bias fp32 [heads, 2 radius + 1] or None."""
+    f = "wd_attention_packed"
+    td = _torch_type(f, dtype)
+    q_rs, k_rs, v_rs = _rows(f, q, td, heads * dh), _rows(f, k, td, kv_heads * dh), _rows(f, v, td, kv_heads * dh, k.shape[0])
+    o_rs = _rows(f, o, "torch.bfloat16", heads * dh, q.shape[0])
+    if k_rs != v_rs:
+        raise ValueError(f"{f}: row strides {k_rs} of k and {v_rs} of v")
+    n_seq = cu_q.numel() - 1
+    _take(f, cu_q, "torch.int32", (n_seq + 1,))
+    _take(f, cu_k, "torch.int32", (n_seq + 1,))
+    radius = 0
+    if bias is not None:
+        radius = (_dims(bias, 2, "bias")[1] - 1) // 2
+        _take(f, bias, "torch.float32", (heads, 2 * radius + 1))
+    _launch(f, (q, k, v, cu_q, cu_k, o, bias), stream, lambda st: _lib.wd_attention_packed(
+        dtype, n_seq, heads, kv_heads, dh, _p(q), q_rs, q.shape[0], _p(cu_q), _p(k), _p(v), k_rs, k.shape[0], _p(cu_k),
+        float(scale), _p(bias), radius, _p(o), o_rs, st))
+
+
+def wd_qknorm_rope_axes(dtype, dh, axes: wd_rope_axes, pos, q, g_q, q_out, k=None, g_k=None, k_out=None, eps=1e-6,
+                        stream=None):
+    """q, q_out [rows, heads*dh], k, k_out [rows, kv_heads*dh] or None, pos int32 [rows, 3],
+    gains fp32 [row width] or None."""
+    f = "wd_qknorm_rope_axes"
+    td = _torch_type(f, dtype)
+    rows, wq = _dims(q, 2, "q")
+    wk = 0 if k is None else _dims(k, 2, "k")[1]
+    if wq % dh or wk % dh:
+        raise ValueError(f"{f}: rows of {wq} and {wk} elements with heads of {dh}")
+    strides = [_rows(f, t, td, w, rows) if t is not None else 0 for t, w in ((q, wq), (q_out, wq), (k, wk), (k_out, wk))]
+    if (k is None) != (k_out is None):
+        raise ValueError(f"{f}: k without k_out, or k_out without k")
+    _take(f, pos, "torch.int32", (rows, 3))
+    for g, w in ((g_q, wq), (g_k, wk)):
+        if g is not None:
+            _take(f, g, "torch.float32", (w,))
+    _launch(f, (q, q_out, pos, k, k_out, g_q, g_k), stream, lambda st: _lib.wd_qknorm_rope_axes(
+        dtype, rows, dh, C.byref(axes), _p(pos), _p(q), strides[0], wq // dh, _p(g_q), _p(q_out), strides[1], _p(k),
+        strides[2], wk // dh, _p(g_k), _p(k_out), strides[3], float(eps), st))
+
+
+def wd_add_norm(x_dtype, x, y_dtype, y, norm, gain, beta, eps, sum, out_dtype, out, scale=None, stream=None):
+    """x, y, sum, out [rows, D] dense (y and sum may be None), gain, beta fp32 [D] or None,
+    scale fp32 [rows] for the e4m3 output (out uint8)."""
+    f = "wd_add_norm"
+    rows, D = _dims(x, 2, "x")
+    for t, td in ((x, x_dtype), (y, y_dtype), (sum, x_dtype), (out, out_dtype)):
+        if t is not None:
+            _take(f, t, _torch_type(f, td), (rows, D))
+    for t, n in ((gain, D), (beta, D), (scale, rows)):
+        if t is not None:
+            _take(f, t, "torch.float32", (n,))
+    _launch(f, (x, y, gain, beta, sum, out, scale), stream, lambda st: _lib.wd_add_norm(
+        rows, D, x_dtype, _p(x), y_dtype, _p(y), norm, _p(gain), _p(beta), float(eps), _p(sum), out_dtype, _p(out),
+        _p(scale), st))
+
+
+def wd_gemm_lora_bytes(M: int, n_seg: int, rank: int) -> int:
+    return _lib.wd_gemm_lora_bytes(M, n_seg, rank)
+
+
+def wd_gemm_lora(M, N, K, A, W, bias, lora: wd_lora, epilogue, out, ws, gate_a=None, gate_b=None, stream=None):
+    """A [M, K], W [N, K] bf16, bias, gates fp32 [N] or None, lora from wd_lora.of, out
+    [M, N] in the epilogue's type, ws at least wd_gemm_lora_bytes bytes."""
+    f = "wd_gemm_lora"
+    _take(f, A, "torch.bfloat16", (M, K))
+    _take(f, W, "torch.bfloat16", (N, K))
+    _take(f, out, {EPI_F32: "torch.float32", EPI_RESID: "torch.float32", EPI_STORE_F16: "torch.float16"}.get(
+        epilogue, "torch.bfloat16"), (M, N))
+    for t in (bias, gate_a, gate_b):
+        if t is not None:
+            _take(f, t, "torch.float32", (N,))
+    seg, adapter, down, up, scale = lora.tensors
+    if down.shape[2] != K or up.shape[1] != N:
+        raise ValueError(f"{f}: adapters of {up.shape[1]} x {down.shape[2]} for a layer of {N} x {K}")
+    _launch(f, (A, W, bias, gate_a, gate_b, out, ws, seg, adapter, down, up, scale), stream, lambda st: _lib.wd_gemm_lora(
+        M, N, K, _p(A), _p(W), _p(bias), C.byref(lora), epilogue, _p(out), _p(gate_a), _p(gate_b), _p(ws),
+        ws.numel() * ws.element_size(), st))
 
 
 def wd_test_exp2(x, y_fma, y_fma2, y_mufu, y_lib, stream=None):

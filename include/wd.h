@@ -55,8 +55,9 @@ typedef enum {
 
 /* WD_F16 (IEEE half) is not a model dtype: it names the cross-attention
  * operands of the WD_BF16 path (the K/V cache and the cross queries) and the
- * operand type accepted by wd_attention. */
-typedef enum { WD_F32 = 0, WD_BF16 = 1, WD_F16 = 2 } wd_dtype;
+ * operand type accepted by wd_attention.  WD_E4M3 names the 8-bit output of
+ * wd_add_norm (codes with one scale per row); no other argument takes it. */
+typedef enum { WD_F32 = 0, WD_BF16 = 1, WD_F16 = 2, WD_E4M3 = 3 } wd_dtype;
 typedef enum { WD_NORM_LAYER = 0, WD_NORM_RMS = 1 } wd_norm;
 
 /* Model and video dimensions.  D = model width, heads x (D/heads) attention
@@ -426,6 +427,129 @@ wd_status wd_quant_rows_e4m3(int dtype, int rows, int K, const void* x, void* q,
 wd_status wd_gemm_fp8(int M, int N, int K, const void* Aq, const float* sa, const void* Bq, const float* sb,
                       const float* bias, int epilogue, void* out, const float* gate_a, const float* gate_b,
                       wd_stream stream);
+
+/* ------------------------------------------------------------------ packed batches
+ * Building blocks for requests of different sizes served in one call: their
+ * rows lie one request behind the other in one buffer, and int32 DEVICE
+ * offsets say where each begins.  The offsets must not decrease; values
+ * outside the buffer count as its nearest end, so no offset makes a kernel
+ * leave its buffers, but results for decreasing offsets are unspecified.
+ * None of these calls reads device memory on the host, so they can be
+ * captured into a CUDA graph, and a replay follows offsets, positions and
+ * adapter ids that were rewritten in place.  Inputs and outputs may not
+ * overlap except where a comment allows it. */
+
+/* Attention within each sequence of a packed batch.  Sequence s owns query
+ * rows cu_q[s] .. cu_q[s+1] - 1 and key rows cu_k[s] .. cu_k[s+1] - 1 (cu_q,
+ * cu_k [n_seq + 1] int32).  For query i and keys j of one sequence, counted
+ * from its first row, and head h:
+ *   t_ij = scale q_i k_j + bias[h, clamp(j - i, -radius, radius) + radius]
+ *   o_i = sum_j softmax_j(t_ij) v_j
+ * - q, o [q_rows, heads*dh] with row strides q_rs, o_rs; k, v [k_rows,
+ *   kv_heads*dh] with row stride kv_rs (elements, multiples of 8, at least the
+ *   row's width), so q, k and v may be the column blocks of one fused buffer.
+ *   heads is a multiple of kv_heads; query head h reads key/value head
+ *   h / (heads / kv_heads).  Self-attention: cu_k = cu_q.
+ * - dtype WD_BF16 or WD_F16 (q, k, v; the probabilities take that type in the
+ *   P V product, statistics and accumulation are fp32); o is bf16.  dh 64 or 128.
+ * - scale > 0 (1/sqrt(dh) for the DiT; a text encoder without it passes 1).
+ * - bias [heads, 2 radius + 1] fp32 with 1 <= radius <= 1024, or NULL with
+ *   radius 0.  Any table by distance fits: beyond the radius the end values
+ *   hold.  -inf leaves a key out (with both ends -inf, a window, whose far key
+ *   blocks are skipped); the value rows of such keys still have to be finite.
+ *   Finite values beyond +-1e30 / log2(e) count as that.
+ * - A row that sees no key (an empty key range, or all of them left out) gives
+ *   zeros.  A row of NaN or +inf scores gives NaN.  Rows of q outside every
+ *   sequence (behind the last one, say) are not computed, and o is left as it
+ *   was there; rows of k and v outside a sequence never reach its output,
+ *   whatever they hold.
+ * Errors: dh or dtype not above -> WD_ERR_UNSUPPORTED / WD_ERR_DTYPE; empty
+ * shapes, heads not a multiple of kv_heads, strides below the width, more than
+ * 2^30 rows, radius out of range -> WD_ERR_SHAPE; scale not finite and positive
+ * -> WD_ERR_ARG; strides not multiples of 8 -> WD_ERR_ALIGN. */
+wd_status wd_attention_packed(int dtype, int n_seq, int heads, int kv_heads, int dh, const void* q, int64_t q_rs,
+                              int64_t q_rows, const int* cu_q, const void* k, const void* v, int64_t kv_rs,
+                              int64_t k_rows, const int* cu_k, float scale, const float* bias, int radius, void* o,
+                              int64_t o_rs, wd_stream stream);
+
+/* Rotary positions with three axes (frame, row, column): HOST struct.  The
+ * first sec[0] channels of a head turn with the frame, the next sec[1] with the
+ * row, the last sec[2] with the column (even numbers, zero allowed, sum dh).
+ * Pair p of a section of d channels turns by
+ *   pos[axis] * step[axis] * theta^(-2p/d),
+ * step (1 for grid indices) stretching an axis.  The DiT's own grid is
+ * sec = {dh - 4 (dh/6), 2 (dh/6), 2 (dh/6)}, theta 10000, step 1 ([I2V] 5.3 (2)). */
+typedef struct {
+  int sec[3];
+  double theta;
+  double step[3];
+} wd_rope_axes;
+
+/* QK-RMSNorm and rotary positions given per token ([I2V] 5.3 (1), (2), for
+ * rows of any grids in any order): for q [rows, heads*dh] and k [rows,
+ * kv_heads*dh],
+ *   out = R(pos[row]) (x / sqrt(mean(x^2) + eps) * g)
+ * with the mean over the whole row (all heads), channel pairs (2p, 2p+1) as (re,
+ * im), pos [rows, 3] int32 (any sign), g_q [heads*dh] and g_k [kv_heads*dh] fp32
+ * or NULL (that tensor is rotated only).  k NULL: q alone (kv_heads, k strides,
+ * g_k and k_out unused).  dtype WD_BF16, WD_F32 or WD_F16; statistics and angles
+ * in fp32 or better (angles exact to 2^-28 turns at any position).  Row strides
+ * q_rs, qo_rs, k_rs, ko_rs in elements, multiples of 8.  q_out may be q (with
+ * qo_rs = q_rs) and k_out may be k; otherwise outputs and inputs may not overlap.
+ * Errors: dh not a multiple of 8 in 8..256, sections that are odd, negative or
+ * do not add up to dh, rows wider than 8192, empty shapes, strides below the
+ * width -> WD_ERR_SHAPE; theta or step not finite and positive, eps < 0 ->
+ * WD_ERR_ARG; strides not multiples of 8 -> WD_ERR_ALIGN. */
+wd_status wd_qknorm_rope_axes(int dtype, int64_t rows, int dh, const wd_rope_axes* axes, const int* pos, const void* q,
+                              int64_t q_rs, int heads, const float* g_q, void* q_out, int64_t qo_rs, const void* k,
+                              int64_t k_rs, int kv_heads, const float* g_k, void* k_out, int64_t ko_rs, float eps,
+                              wd_stream stream);
+
+/* Residual addition and norm in one pass, per row of x, y [rows, D] (dense):
+ *   s = x + y (fp32; y NULL: s = x),  n = norm(s) gain + beta,
+ * norm = WD_NORM_RMS (s / sqrt(mean(s^2) + eps)) or WD_NORM_LAYER (mean
+ * subtracted first); gain and beta [D] fp32 or NULL.  sum (x's type, may be x;
+ * NULL: not stored) receives s rounded once; the norm reads the unrounded s.
+ * out [rows, D]: out_dtype WD_F32, WD_BF16, or WD_E4M3 (one byte each, with
+ * scale [rows] fp32: the codes and scales that wd_quant_rows_e4m3 gives for n,
+ * the A operand of wd_gemm_fp8; scale is unused and may be NULL otherwise).
+ * x_dtype and y_dtype WD_F32 or WD_BF16.  D a multiple of 8, at most 8192.
+ * Errors: WD_ERR_DTYPE; empty shapes or D -> WD_ERR_SHAPE; an unknown norm or
+ * eps < 0 -> WD_ERR_ARG. */
+wd_status wd_add_norm(int64_t rows, int D, int x_dtype, const void* x, int y_dtype, const void* y, int norm,
+                      const float* gain, const float* beta, float eps, void* sum, int out_dtype, void* out,
+                      float* scale, wd_stream stream);
+
+/* Low-rank adapters of the requests in a packed batch: HOST struct of device
+ * pointers.  Request s owns rows seg[s] .. seg[s+1] - 1 (seg [n_seg + 1]) and
+ * uses adapter adapter[s] (int32 [n_seg]; any value outside [0, n_adapters)
+ * means none; several requests may share one).  Rows outside every request have
+ * no adapter.  down [n_adapters, rank, K] and up [n_adapters, N, rank] bf16,
+ * scale [n_adapters] fp32 or NULL (1).  rank a multiple of 8 in 8..256 (smaller
+ * ranks are padded with zeros). */
+typedef struct {
+  int n_seg, n_adapters, rank;
+  const int *seg, *adapter;
+  const void *down, *up;
+  const float* scale;
+} wd_lora;
+
+/* Workspace bytes of wd_gemm_lora (0 for sizes it refuses). */
+size_t wd_gemm_lora_bytes(int M, int n_seg, int rank);
+
+/* The Linear layer of wd_gemm with each row's own adapter:
+ *   v[m, :] = A[m, :] W^T + bias + scale[a] (A[m, :] down[a]^T) up[a]^T,
+ * a the adapter of row m's request, then wd_gemm's epilogues (0, 1, 2, 3, 5) on v.
+ * A [M, K], W [N, K] bf16 dense, N a multiple of 64, K a multiple of 8.  The
+ * rank-wide middle A down^T is summed in fp32 and enters the second product
+ * rounded to bf16 for 2-byte outputs, and as a sum of two bf16 parts (2^-17) for
+ * fp32 outputs (epilogues 2 and 3).  ws: wd_gemm_lora_bytes(M, n_seg, rank)
+ * bytes, not shared with a call that may run at the same time.
+ * Errors: N, K, rank, n_seg (1 .. 65536), n_adapters < 1, M above 2^29,
+ * n_adapters*N above 2^31 - 1 -> WD_ERR_SHAPE; the workspace -> WD_ERR_WORKSPACE. */
+wd_status wd_gemm_lora(int M, int N, int K, const void* A, const void* W, const float* bias, const wd_lora* lora,
+                       int epilogue, void* out, const float* gate_a, const float* gate_b, void* ws, size_t ws_bytes,
+                       wd_stream stream);
 
 /* ------------------------------------------------------------------ test hooks
  * Two entry points that exist only so that tests can reach pieces of the
