@@ -12,8 +12,16 @@
 namespace wd {
 namespace rows {
 
+// A row is held by wpr = 1, 2, 4 or 8 warps of a 256-thread block, each lane with NV
+// <= 4 chunks of 8 elements: few registers a thread, so that four blocks share an SM
+// and their loads cover one another's arithmetic.
 constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int NV = 8;   // 8-element chunks that a lane holds of its row, at most
+constexpr int MAX_NV = 4, ROW_MAX = MAX_NV * 8 * THREADS;   // widest row: 8192
+
+// Waits for the wpr warps of one row (barrier 1 + the row's place in the block).
+__device__ __forceinline__ void row_sync(int group, int wpr) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(wpr * 32) : "memory");
+}
 
 // Eight consecutive elements of type T as fp32 (16-byte accesses; the cache
 // hint is "streaming": nothing here is read twice).
@@ -72,21 +80,21 @@ __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// Sum (or maximum) of one value per lane over the WPR warps of a row; `red` has one
-// float per warp and is reused: a second reduction of the same loop pass needs another one.
-template <int WPR, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* red, int warp) {
+// Sum (or maximum) of one value per lane over the wpr warps of a row; `red` has one
+// float per warp and serves one reduction.
+template <bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* red, int warp, int wpr) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float w = __shfl_xor_sync(0xffffffffu, v, o);
     v = MAX ? fmaxf(v, w) : v + w;
   }
-  if constexpr (WPR > 1) {
+  if (wpr > 1) {
+    const int group = warp / wpr;
     if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    v = red[warp / WPR * WPR];
-#pragma unroll
-    for (int i = 1; i < WPR; ++i) v = MAX ? fmaxf(v, red[warp / WPR * WPR + i]) : v + red[warp / WPR * WPR + i];
+    row_sync(group, wpr);
+    v = red[group * wpr];
+    for (int i = 1; i < wpr; ++i) v = MAX ? fmaxf(v, red[group * wpr + i]) : v + red[group * wpr + i];
   }
   return v;
 }
@@ -109,8 +117,7 @@ struct RopeArgs {
   void* out[2];
   const float* gain[2];
   int64_t in_rs[2], out_rs[2];
-  int D[2];                           // heads * dh of each tensor
-  int tensors;                        // 1: q only, 2: q and k
+  int D[2];                           // heads * dh of each tensor; 0: not given
   int64_t rows;
   int dh, p1, p2;                     // pairs [0, p1) frame, [p1, p2) row, [p2, dh / 2) column
   float eps;
@@ -127,83 +134,76 @@ __device__ __forceinline__ float2 turn(int pos, uint64_t f) {
   return (quad & 2u) ? make_float2(-a, -b) : make_float2(a, b);
 }
 
-// WPR warps hold one row of one tensor; a block of 8 warps takes 8 / (WPR *
-// tensors) tokens at a time, whose cosines and sines all its warps share in
-// shared memory: dh / 2 of them a token against heads * dh / 2 rotations each
-// in q and k.  The row's loads are issued before the angles are computed.
-template <typename T, int WPR>
-__global__ void __launch_bounds__(THREADS) k_qknorm_rope_axes(const __grid_constant__ RopeArgs a) {
-  __shared__ uint64_t freq[MAX_PAIRS];
-  __shared__ __align__(16) float2 cs[2][WARPS / WPR][MAX_PAIRS];
+// A block takes 8 / wpr tokens, q and k of each in the same warps, and computes the
+// tokens' cosines and sines once into shared memory: dh / 2 of them a token against
+// heads * dh / 2 rotations each in q and k.  The rows' loads are issued first.
+template <typename T, int NV>
+__global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : (NV == 4 ? 3 : 4)) k_qknorm_rope_axes(const __grid_constant__ RopeArgs a, int wpr) {
+  __shared__ __align__(16) float2 cs[WARPS * MAX_PAIRS];   // [token][pair]
   __shared__ float red[2][WARPS];
   const int half = a.dh >> 1;
-  for (int i = threadIdx.x; i < half; i += THREADS) freq[i] = a.freq[i];
-  __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = warp / WPR, in_row = (warp % WPR) * 32 + lane;
-  const int tokens = WARPS / WPR / a.tensors;            // of one pass of the block
-  const int which = a.tensors == 2 ? unit & 1 : 0, mine = a.tensors == 2 ? unit >> 1 : unit;
-  const int D = a.D[which];
-  const float* gain = a.gain[which];
-  int buf = 0;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens; row0 < a.rows;
-       row0 += static_cast<int64_t>(gridDim.x) * tokens, buf ^= 1) {
-    const int64_t row = row0 + mine;
-    const bool live = row < a.rows;
-    const T* x = static_cast<const T*>(a.in[which]) + row * a.in_rs[which];
-    Chunk<T> ch[NV];
+  const int tokens = WARPS / wpr, mine = warp / wpr, in_row = (warp % wpr) * 32 + lane;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens, row = row0 + mine;
+  const bool live = row < a.rows;
+  Chunk<T> ch[2][NV];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const T* x = static_cast<const T*>(a.in[t]) + row * a.in_rs[t];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * WPR * 32 + in_row) * 8;
-      if (live && c < D) ch[i].load(x + c);
+      const int c = (i * wpr * 32 + in_row) * 8;
+      if (live && c < a.D[t]) ch[t][i].load(x + c);
     }
-    for (int i = threadIdx.x; i < tokens * half; i += THREADS) {
-      const int tk = i / half, p = i - tk * half;
-      if (row0 + tk < a.rows)
-        cs[buf][tk][p] = turn(a.pos[(row0 + tk) * 3 + (p < a.p1 ? 0 : (p < a.p2 ? 1 : 2))], freq[p]);
-    }
-    float r = 1.f;
-    if (gain) {   // the same for a whole tensor; with WPR > 1 a unit's warps agree, the others wait below
-      float ss = 0.f;
+  }
+  for (int i = threadIdx.x; i < tokens * half; i += THREADS) {
+    const int tk = i / half, p = i - tk * half;
+    if (row0 + tk < a.rows)
+      cs[i] = turn(a.pos[(row0 + tk) * 3 + (p < a.p1 ? 0 : (p < a.p2 ? 1 : 2))], a.freq[p]);
+  }
+  float r[2] = {1.f, 1.f};
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * WPR * 32 + in_row) * 8;
-        if (live && c < D) {
-          float v[8];
-          ch[i].get(v);
+  for (int t = 0; t < 2; ++t) {
+    if (!a.gain[t]) continue;
+    float ss = 0.f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) ss += v[k] * v[k];
-        }
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * wpr * 32 + in_row) * 8;
+      if (live && c < a.D[t]) {
+        float v[8];
+        ch[t][i].get(v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss += v[k] * v[k];
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      r = ss;
-      if (WPR > 1 && lane == 0) red[buf][warp] = ss;
     }
-    __syncthreads();   // the angles (and the warps' sums); the other buffers serve the next pass
-    if (!live) continue;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0) red[t][warp] = ss;
+  }
+  __syncthreads();   // the angles, and the warps' sums
+  if (!live) return;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float* gain = a.gain[t];
     if (gain) {
-      if constexpr (WPR > 1) {
-        r = 0.f;
-#pragma unroll
-        for (int i = 0; i < WPR; ++i) r += red[buf][unit * WPR + i];
-      }
-      r = rsqrtf(r / D + a.eps);
+      float ss = 0.f;
+      for (int i = 0; i < wpr; ++i) ss += red[t][mine * wpr + i];
+      r[t] = rsqrtf(ss / a.D[t] + a.eps);
     }
-    T* y = static_cast<T*>(a.out[which]) + row * a.out_rs[which];
+    T* y = static_cast<T*>(a.out[t]) + row * a.out_rs[t];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * WPR * 32 + in_row) * 8;
-      if (c >= D) break;
+      const int c = (i * wpr * 32 + in_row) * 8;
+      if (c >= a.D[t]) break;
       float v[8];
-      ch[i].get(v);
+      ch[t][i].get(v);
       if (gain) {
         float g[8];
         load8f(gain + c, g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = v[k] * r * g[k];
+        for (int k = 0; k < 8; ++k) v[k] = v[k] * r[t] * g[k];
       }
-      const float4* t4 = reinterpret_cast<const float4*>(&cs[buf][mine][(c % a.dh) >> 1]);
+      const float4* t4 = reinterpret_cast<const float4*>(&cs[mine * half + ((c % a.dh) >> 1)]);
       const float4 ta = t4[0], tb = t4[1];
       const float co[4] = {ta.x, ta.z, tb.x, tb.z}, si[4] = {ta.y, ta.w, tb.y, tb.w};
       float o[8];
@@ -233,36 +233,36 @@ struct AddNormArgs {
   float eps;
 };
 
-template <typename TX, typename TY, typename TO, int WPR>
-__global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a) {
+template <typename TX, typename TY, typename TO, int NV>
+__global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a, int wpr) {
   constexpr bool Q = std::is_same<TO, uint8_t>::value;
   __shared__ float red[3][WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int in_row = (warp % WPR) * 32 + lane;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (WARPS / WPR) + warp / WPR;
-  const bool live = row < a.rows;   // no early return: the reductions below are the whole block's
+  const int in_row = (warp % wpr) * 32 + lane;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (WARPS / wpr) + warp / wpr;
+  if (row >= a.rows) return;        // the row's warps leave together
   const int D = a.D;
-  const int64_t base = live ? row * D : 0;
+  const int64_t base = row * D;
   float v[NV][8];
   {
     Chunk<TX> cx[NV];
     Chunk<TY> cy[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * WPR * 32 + in_row) * 8;
-      if (live && c < D) cx[i].load(static_cast<const TX*>(a.x) + base + c);
+      const int c = (i * wpr * 32 + in_row) * 8;
+      if (c < D) cx[i].load(static_cast<const TX*>(a.x) + base + c);
     }
     if (a.y) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * WPR * 32 + in_row) * 8;
-        if (live && c < D) cy[i].load(static_cast<const TY*>(a.y) + base + c);
+        const int c = (i * wpr * 32 + in_row) * 8;
+        if (c < D) cy[i].load(static_cast<const TY*>(a.y) + base + c);
       }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * WPR * 32 + in_row) * 8;
-      if (live && c < D) {
+      const int c = (i * wpr * 32 + in_row) * 8;
+      if (c < D) {
         cx[i].get(v[i]);
         if (a.y) {
           float w[8];
@@ -284,12 +284,12 @@ __global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) s += v[i][k];
-    mean = row_reduce<WPR, false>(s, red[0], warp) / D;
+    mean = row_reduce<false>(s, red[0], warp, wpr) / D;
   }
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * WPR * 32 + in_row) * 8;
+    const int c = (i * wpr * 32 + in_row) * 8;
     if (c < D) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -298,11 +298,11 @@ __global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a) {
       }
     }
   }
-  const float rstd = rsqrtf(row_reduce<WPR, false>(q, red[1], warp) / D + a.eps);
+  const float rstd = rsqrtf(row_reduce<false>(q, red[1], warp, wpr) / D + a.eps);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * WPR * 32 + in_row) * 8;
+    const int c = (i * wpr * 32 + in_row) * 8;
     if (c < D) {
       float g[8];
       if (a.gain) {
@@ -321,18 +321,17 @@ __global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a) {
       if constexpr (Q) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[i][k]));
-      } else if (live) {
+      } else {
         Chunk<TO>::store(static_cast<TO*>(a.out) + base + c, v[i]);
       }
     }
   }
   if constexpr (Q) {
-    amax = row_reduce<WPR, true>(amax, red[2], warp);
+    amax = row_reduce<true>(amax, red[2], warp, wpr);
     const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-    if (!live) return;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * WPR * 32 + in_row) * 8;
+      const int c = (i * wpr * 32 + in_row) * 8;
       if (c < D) {
         uint32_t w[2] = {0u, 0u};
 #pragma unroll
@@ -350,29 +349,41 @@ __global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a) {
 }  // namespace rows
 
 // ------------------------------------------------------------------ host side
-constexpr int ROW_MAX = rows::NV * 8 * 32 * 4;   // 8192: four warps a row
+// Warps a row of D elements takes, with at most MAX_NV chunks a lane.
+static int row_warps(int D) {
+  int w = 1;
+  while (w * 32 * rows::MAX_NV * 8 < D) w *= 2;
+  return w;
+}
+
+// f(integral constant NV) for the chunks a lane of wpr warps needs for D elements.
+template <typename F>
+static void row_chunks(int D, int wpr, F&& f) {
+  switch ((D + wpr * 256 - 1) / (wpr * 256)) {
+    case 1: f(std::integral_constant<int, 1>()); break;
+    case 2: f(std::integral_constant<int, 2>()); break;
+    case 3: f(std::integral_constant<int, 3>()); break;
+    default: f(std::integral_constant<int, 4>()); break;
+  }
+}
 
 template <typename T>
 static wd_status qknorm_rope_axes(const rows::RopeArgs& a, cudaStream_t st) {
-  const int D = a.tensors == 2 && a.D[1] > a.D[0] ? a.D[1] : a.D[0];
-  const int wpr = D <= rows::NV * 8 * 32 ? 1 : 4;
-  const int tokens = rows::WARPS / wpr / a.tensors;
-  const int64_t want = (a.rows + tokens - 1) / tokens, most = static_cast<int64_t>(sm_count()) * 8;
-  const unsigned grid = static_cast<unsigned>(want < most ? want : most);
+  const int D = a.D[1] > a.D[0] ? a.D[1] : a.D[0], wpr = row_warps(D), tokens = rows::WARPS / wpr;
   Trace tr(KC_ROPE, st);
-  if (wpr == 1) rows::k_qknorm_rope_axes<T, 1><<<grid, rows::THREADS, 0, st>>>(a);
-  else rows::k_qknorm_rope_axes<T, 4><<<grid, rows::THREADS, 0, st>>>(a);
+  row_chunks(D, wpr, [&](auto nv) {
+    rows::k_qknorm_rope_axes<T, nv()><<<static_cast<unsigned>((a.rows + tokens - 1) / tokens), rows::THREADS, 0, st>>>(a, wpr);
+  });
   return launch_status("qknorm_rope_axes");
 }
 
 template <typename TX, typename TY, typename TO>
 static wd_status add_norm_t(const rows::AddNormArgs& a, cudaStream_t st) {
-  const int wpr = a.D <= rows::NV * 8 * 32 ? 1 : 4;
-  const int64_t grid = (a.rows + rows::WARPS / wpr - 1) / (rows::WARPS / wpr);
-  if (grid > 0x7fffffff) { set_error("add_norm: %lld rows", (long long)a.rows); return WD_ERR_SHAPE; }
+  const int wpr = row_warps(a.D), rpb = rows::WARPS / wpr;
   Trace tr(KC_NORM, st);
-  if (wpr == 1) rows::k_add_norm<TX, TY, TO, 1><<<static_cast<unsigned>(grid), rows::THREADS, 0, st>>>(a);
-  else rows::k_add_norm<TX, TY, TO, 4><<<static_cast<unsigned>(grid), rows::THREADS, 0, st>>>(a);
+  row_chunks(a.D, wpr, [&](auto nv) {
+    rows::k_add_norm<TX, TY, TO, nv()><<<static_cast<unsigned>((a.rows + rpb - 1) / rpb), rows::THREADS, 0, st>>>(a, wpr);
+  });
   return launch_status("add_norm");
 }
 

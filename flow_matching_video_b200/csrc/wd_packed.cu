@@ -18,13 +18,14 @@ static wd_status check_stride(const char* what, int64_t rs, int64_t width) {
 
 static bool positive(double x) { return std::isfinite(x) && x > 0; }
 
-// step * theta^(-2p/d) / 2 pi mod 1 of one pair, in 2^-64 turns.
-static uint64_t turn_fraction(double theta, double step, int p, int d) {
-  const long double two_pi = 6.283185307179586476925286766559006L;
-  const long double f = step * powl(theta, -2.0L * p / d) / two_pi;
-  const long double frac = f - floorl(f);
-  const long double scaled = roundl(ldexpl(frac, 64));
-  return scaled >= 18446744073709551616.0L ? 0 : static_cast<uint64_t>(scaled);
+// The pairs of one section: step * theta^(-2p/d) / 2 pi mod 1 in 2^-64 turns for p = 0 ..
+// d/2 - 1, by repeated products in extended precision (64 of them keep 2^-57 of the value).
+static void turn_fractions(double theta, double step, int d, uint64_t* out) {
+  if (d == 0) return;
+  const long double ratio = powl(theta, -2.0L / d);
+  long double f = step / 6.283185307179586476925286766559006L;
+  for (int p = 0; p < d / 2; ++p, f *= ratio)
+    out[p] = static_cast<uint64_t>((f < 1 ? f : f - floorl(f)) * 18446744073709551616.0L);
 }
 
 }  // namespace wd
@@ -94,13 +95,12 @@ wd_status wd_qknorm_rope_axes(int dtype, int64_t rows, int dh, const wd_rope_axe
   }
   rows::RopeArgs a{};
   a.pos = pos; a.rows = rows; a.dh = dh; a.eps = eps;
-  a.tensors = k ? 2 : 1;
   a.p1 = axes->sec[0] / 2; a.p2 = a.p1 + axes->sec[1] / 2;
   a.in[0] = q; a.out[0] = q_out; a.gain[0] = g_q; a.in_rs[0] = q_rs; a.out_rs[0] = qo_rs;
   a.in[1] = k; a.out[1] = k_out; a.gain[1] = g_k; a.in_rs[1] = k_rs; a.out_rs[1] = ko_rs;
-  for (int i = 0; i < a.tensors; ++i) {
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
     const int64_t n = i ? kv_heads : heads;
-    if (n <= 0 || n * dh > ROW_MAX) { set_error("qknorm_rope_axes: %lld heads of %d (rows up to %d wide)", (long long)n, dh, ROW_MAX); return WD_ERR_SHAPE; }
+    if (n <= 0 || n * dh > rows::ROW_MAX) { set_error("qknorm_rope_axes: %lld heads of %d (rows up to %d wide)", (long long)n, dh, rows::ROW_MAX); return WD_ERR_SHAPE; }
     a.D[i] = static_cast<int>(n) * dh;
     WD_TRY(check_stride(i ? "qknorm_rope_axes k" : "qknorm_rope_axes q", a.in_rs[i], a.D[i]));
     WD_TRY(check_stride(i ? "qknorm_rope_axes k_out" : "qknorm_rope_axes q_out", a.out_rs[i], a.D[i]));
@@ -109,9 +109,11 @@ wd_status wd_qknorm_rope_axes(int dtype, int64_t rows, int dh, const wd_rope_axe
       return WD_ERR_ARG;
     }
   }
-  for (int p = 0; p < dh / 2; ++p) {
-    const int ax = p < a.p1 ? 0 : (p < a.p2 ? 1 : 2);
-    a.freq[p] = turn_fraction(axes->theta, axes->step[ax], p - (ax == 0 ? 0 : (ax == 1 ? a.p1 : a.p2)), axes->sec[ax]);
+  for (int i = 0, p = 0; i < 3; p += axes->sec[i++] / 2) {
+    if (i && axes->sec[i] == axes->sec[i - 1] && axes->step[i] == axes->step[i - 1])   // rows and columns, as a rule
+      memcpy(a.freq + p, a.freq + p - axes->sec[i] / 2, axes->sec[i] / 2 * sizeof(a.freq[0]));
+    else
+      turn_fractions(axes->theta, axes->step[i], axes->sec[i], a.freq + p);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == WD_BF16) return qknorm_rope_axes<bf16>(a, st);
@@ -129,8 +131,8 @@ wd_status wd_add_norm(int64_t rows, int D, int x_dtype, const void* x, int y_dty
     return WD_ERR_DTYPE;
   }
   if (out_dtype == WD_E4M3) { WD_NEED(scale); }
-  if (rows <= 0 || rows > MAX_ROWS || D <= 0 || D % 8 || D > ROW_MAX) {
-    set_error("add_norm: rows=%lld, D=%d (a multiple of 8 up to %d)", (long long)rows, D, ROW_MAX);
+  if (rows <= 0 || rows > MAX_ROWS || D <= 0 || D % 8 || D > rows::ROW_MAX) {
+    set_error("add_norm: rows=%lld, D=%d (a multiple of 8 up to %d)", (long long)rows, D, rows::ROW_MAX);
     return WD_ERR_SHAPE;
   }
   if ((norm != WD_NORM_LAYER && norm != WD_NORM_RMS) || !(eps >= 0.f) || !std::isfinite(eps)) {

@@ -75,15 +75,16 @@ class wd_lora(C.Structure):
         """Adapters of a packed batch: seg [n_seg + 1] and adapter [n_seg] int32, down
         [n_adapters, rank, K] and up [n_adapters, N, rank] bf16, scale [n_adapters]
         fp32 or None; dense tensors of one device, which the struct keeps alive."""
+        f = "wd_lora"
         na, r, k = _dims(down, 3, "down")
         n = _dims(up, 3, "up")[1]
         ns = adapter.numel()
-        _take("wd_lora", seg, "torch.int32", (ns + 1,))
-        _take("wd_lora", adapter, "torch.int32", (ns,))
-        _take("wd_lora", down, "torch.bfloat16", (na, r, k))
-        _take("wd_lora", up, "torch.bfloat16", (na, n, r))
+        _take(f, seg, _torch_type(f, "i32"), (ns + 1,))
+        _take(f, adapter, _torch_type(f, "i32"), (ns,))
+        _take(f, down, _torch_type(f, WD_BF16), (na, r, k))
+        _take(f, up, _torch_type(f, WD_BF16), (na, n, r))
         if scale is not None:
-            _take("wd_lora", scale, "torch.float32", (na,))
+            _take(f, scale, _torch_type(f, WD_F32), (na,))
         out = cls(ns, na, r, _p(seg), _p(adapter), _p(down), _p(up), _p(scale))
         out.tensors = (seg, adapter, down, up, scale)
         return out
@@ -169,43 +170,55 @@ def _ok(status: int, where: str):
 def _dims(t, n, name):
     if t.dim() != n:
         raise ValueError(f"{name}: {t.dim()} dimensions, not {n}")
-    return tuple(t.shape)
+    return t.shape
 
 
 def _take(where, t, dtype, shape):
-    """A dense tensor of this element type (by name) and shape."""
-    if str(t.dtype) != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    """A dense tensor of this element type and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: a dense {dtype} tensor {list(shape)} is wanted, not {t.dtype} {list(t.shape)}"
                          f" with strides {list(t.stride())}")
 
 
 def _rows(where, t, dtype, width, rows=None):
     """Row stride of a 2D tensor [rows, width] whose rows are dense."""
-    if str(t.dtype) != dtype or t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows) or \
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows) or \
             (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{where}: {dtype} rows of {width} dense elements are wanted, not {t.dtype} {list(t.shape)}"
+        raise ValueError(f"{where}: {dtype} rows of {width} dense elements are wanted, not {t.dtype} {list(shape)}"
                          f" with strides {list(t.stride())}")
-    return t.stride(0) if t.shape[0] > 1 else width
+    return t.stride(0) if shape[0] > 1 else width
 
 
-_TORCH = {WD_F32: "torch.float32", WD_BF16: "torch.bfloat16", WD_F16: "torch.float16", WD_E4M3: "torch.uint8"}
+_torch_types = {}
 
 
 def _torch_type(where, dtype):
-    if dtype not in _TORCH:
+    """The torch type of a WD_* dtype."""
+    if not _torch_types:
+        import torch
+        _torch_types.update({WD_F32: torch.float32, WD_BF16: torch.bfloat16, WD_F16: torch.float16, WD_E4M3: torch.uint8,
+                             "i32": torch.int32})
+    if dtype not in _torch_types:
         raise ValueError(f"{where}: dtype {dtype}")
-    return _TORCH[dtype]
+    return _torch_types[dtype]
 
 
 def _launch(where, tensors, stream, call):
     """call(stream handle) on the tensors' own device: its current stream, or the one given."""
     import torch
-    live = [t for t in tensors if t is not None]
-    dev = live[0].device
-    if any(t.device != dev for t in live) or dev.type != "cuda":
-        raise ValueError(f"{where}: tensors on {sorted({str(t.device) for t in live})}, one CUDA device is wanted")
-    with torch.cuda.device(dev):
-        _ok(call(_stream(stream)), where)
+    live = [t.get_device() for t in tensors if t is not None]
+    if live[0] < 0 or live.count(live[0]) != len(live):
+        raise ValueError(f"{where}: tensors on {sorted({str(t.device) for t in tensors if t is not None})}, one CUDA"
+                         " device is wanted")
+    # the stream's handle without a Stream object: 0.1 us instead of 3
+    st = torch._C._cuda_getCurrentRawStream(live[0]) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == live[0]:
+        status = call(st)
+    else:
+        with torch.cuda.device(live[0]):
+            status = call(st)
+    _ok(status, where)
 
 
 def make_dims(d) -> wd_dims:
@@ -345,16 +358,16 @@ def wd_attention_packed(dtype, heads, kv_heads, dh, q, k, v, cu_q, cu_k, scale, 
     f = "wd_attention_packed"
     td = _torch_type(f, dtype)
     q_rs, k_rs, v_rs = _rows(f, q, td, heads * dh), _rows(f, k, td, kv_heads * dh), _rows(f, v, td, kv_heads * dh, k.shape[0])
-    o_rs = _rows(f, o, "torch.bfloat16", heads * dh, q.shape[0])
+    o_rs = _rows(f, o, _torch_type(f, WD_BF16), heads * dh, q.shape[0])
     if k_rs != v_rs:
         raise ValueError(f"{f}: row strides {k_rs} of k and {v_rs} of v")
     n_seq = cu_q.numel() - 1
-    _take(f, cu_q, "torch.int32", (n_seq + 1,))
-    _take(f, cu_k, "torch.int32", (n_seq + 1,))
+    _take(f, cu_q, _torch_type(f, "i32"), (n_seq + 1,))
+    _take(f, cu_k, _torch_type(f, "i32"), (n_seq + 1,))
     radius = 0
     if bias is not None:
         radius = (_dims(bias, 2, "bias")[1] - 1) // 2
-        _take(f, bias, "torch.float32", (heads, 2 * radius + 1))
+        _take(f, bias, _torch_type(f, WD_F32), (heads, 2 * radius + 1))
     _launch(f, (q, k, v, cu_q, cu_k, o, bias), stream, lambda st: _lib.wd_attention_packed(
         dtype, n_seq, heads, kv_heads, dh, _p(q), q_rs, q.shape[0], _p(cu_q), _p(k), _p(v), k_rs, k.shape[0], _p(cu_k),
         float(scale), _p(bias), radius, _p(o), o_rs, st))
@@ -373,10 +386,10 @@ def wd_qknorm_rope_axes(dtype, dh, axes: wd_rope_axes, pos, q, g_q, q_out, k=Non
     strides = [_rows(f, t, td, w, rows) if t is not None else 0 for t, w in ((q, wq), (q_out, wq), (k, wk), (k_out, wk))]
     if (k is None) != (k_out is None):
         raise ValueError(f"{f}: k without k_out, or k_out without k")
-    _take(f, pos, "torch.int32", (rows, 3))
+    _take(f, pos, _torch_type(f, "i32"), (rows, 3))
     for g, w in ((g_q, wq), (g_k, wk)):
         if g is not None:
-            _take(f, g, "torch.float32", (w,))
+            _take(f, g, _torch_type(f, WD_F32), (w,))
     _launch(f, (q, q_out, pos, k, k_out, g_q, g_k), stream, lambda st: _lib.wd_qknorm_rope_axes(
         dtype, rows, dh, C.byref(axes), _p(pos), _p(q), strides[0], wq // dh, _p(g_q), _p(q_out), strides[1], _p(k),
         strides[2], wk // dh, _p(g_k), _p(k_out), strides[3], float(eps), st))
@@ -392,7 +405,7 @@ def wd_add_norm(x_dtype, x, y_dtype, y, norm, gain, beta, eps, sum, out_dtype, o
             _take(f, t, _torch_type(f, td), (rows, D))
     for t, n in ((gain, D), (beta, D), (scale, rows)):
         if t is not None:
-            _take(f, t, "torch.float32", (n,))
+            _take(f, t, _torch_type(f, WD_F32), (n,))
     _launch(f, (x, y, gain, beta, sum, out, scale), stream, lambda st: _lib.wd_add_norm(
         rows, D, x_dtype, _p(x), y_dtype, _p(y), norm, _p(gain), _p(beta), float(eps), _p(sum), out_dtype, _p(out),
         _p(scale), st))
@@ -406,13 +419,13 @@ def wd_gemm_lora(M, N, K, A, W, bias, lora: wd_lora, epilogue, out, ws, gate_a=N
     """A [M, K], W [N, K] bf16, bias, gates fp32 [N] or None, lora from wd_lora.of, out
     [M, N] in the epilogue's type, ws at least wd_gemm_lora_bytes bytes."""
     f = "wd_gemm_lora"
-    _take(f, A, "torch.bfloat16", (M, K))
-    _take(f, W, "torch.bfloat16", (N, K))
-    _take(f, out, {EPI_F32: "torch.float32", EPI_RESID: "torch.float32", EPI_STORE_F16: "torch.float16"}.get(
-        epilogue, "torch.bfloat16"), (M, N))
+    _take(f, A, _torch_type(f, WD_BF16), (M, K))
+    _take(f, W, _torch_type(f, WD_BF16), (N, K))
+    _take(f, out, _torch_type(f, WD_F32 if epilogue in (EPI_F32, EPI_RESID) else
+                              WD_F16 if epilogue == EPI_STORE_F16 else WD_BF16), (M, N))
     for t in (bias, gate_a, gate_b):
         if t is not None:
-            _take(f, t, "torch.float32", (N,))
+            _take(f, t, _torch_type(f, WD_F32), (N,))
     seg, adapter, down, up, scale = lora.tensors
     if down.shape[2] != K or up.shape[1] != N:
         raise ValueError(f"{f}: adapters of {up.shape[1]} x {down.shape[2]} for a layer of {N} x {K}")
