@@ -134,85 +134,96 @@ __device__ __forceinline__ float2 turn(int pos, uint64_t f) {
   return (quad & 2u) ? make_float2(-a, -b) : make_float2(a, b);
 }
 
-// A block takes 8 / wpr tokens, q and k of each in the same warps, and computes the
-// tokens' cosines and sines once into shared memory: dh / 2 of them a token against
-// heads * dh / 2 rotations each in q and k.  The rows' loads are issued first.
-template <typename T, int NV>
-__global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : (NV == 4 ? 3 : 4)) k_qknorm_rope_axes(const __grid_constant__ RopeArgs a, int wpr) {
+// wpr warps take one token, q and then k in the same lanes, and compute the token's
+// cosines and sines once into shared memory: dh / 2 of them against heads * dh / 2
+// rotations each in q and k.  The rows' loads are issued first.  With SAME (dh
+// divides wpr * 256) all chunks of a lane lie at one place of their heads: its four
+// cosines and sines are read once, with the row's 1 / rms multiplied in.
+template <typename T, int NV, bool SAME>
+__global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : (NV == 4 ? 3 : 4))
+k_qknorm_rope_axes(const __grid_constant__ RopeArgs a, int wpr) {
   __shared__ __align__(16) float2 cs[WARPS * MAX_PAIRS];   // [token][pair]
   __shared__ float red[2][WARPS];
   const int half = a.dh >> 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tokens = WARPS / wpr, mine = warp / wpr, in_row = (warp % wpr) * 32 + lane;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens, row = row0 + mine;
-  const bool live = row < a.rows;
+  const int mine = warp / wpr, in_row = (warp - mine * wpr) * 32 + lane;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (WARPS / wpr) + mine;
+  if (row >= a.rows) return;   // the token's warps leave together
   Chunk<T> ch[2][NV];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const T* x = static_cast<const T*>(a.in[t]) + row * a.in_rs[t];
+    const T* x = static_cast<const T*>(a.in[t]) + row * a.in_rs[t] + in_row * 8;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * wpr * 32 + in_row) * 8;
-      if (live && c < a.D[t]) ch[t][i].load(x + c);
-    }
+    for (int i = 0; i < NV; ++i)
+      if ((i * wpr * 32 + in_row) * 8 < a.D[t]) ch[t][i].load(x + i * wpr * 256);
   }
-  for (int i = threadIdx.x; i < tokens * half; i += THREADS) {
-    const int tk = i / half, p = i - tk * half;
-    if (row0 + tk < a.rows)
-      cs[i] = turn(a.pos[(row0 + tk) * 3 + (p < a.p1 ? 0 : (p < a.p2 ? 1 : 2))], a.freq[p]);
-  }
-  float r[2] = {1.f, 1.f};
+  float2* tab = cs + mine * half;
+  for (int p = in_row; p < half; p += wpr * 32)
+    tab[p] = turn(a.pos[row * 3 + (p < a.p1 ? 0 : (p < a.p2 ? 1 : 2))], a.freq[p]);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     if (!a.gain[t]) continue;
-    float ss = 0.f;
+    float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * wpr * 32 + in_row) * 8;
-      if (live && c < a.D[t]) {
+      if ((i * wpr * 32 + in_row) * 8 < a.D[t]) {
         float v[8];
         ch[t][i].get(v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ss += v[k] * v[k];
+        for (int k = 0; k < 8; k += 2) ss = ffma2(make_float2(v[k], v[k + 1]), make_float2(v[k], v[k + 1]), ss);
       }
     }
+    float s = ss.x + ss.y;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (lane == 0) red[t][warp] = ss;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red[t][warp] = s;
   }
-  __syncthreads();   // the angles, and the warps' sums
-  if (!live) return;
+  row_sync(mine, wpr);   // the angles, and the warps' sums
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const float* gain = a.gain[t];
+    const float* gain = a.gain[t] ? a.gain[t] + in_row * 8 : nullptr;
+    float r = 1.f;
     if (gain) {
-      float ss = 0.f;
-      for (int i = 0; i < wpr; ++i) ss += red[t][mine * wpr + i];
-      r[t] = rsqrtf(ss / a.D[t] + a.eps);
+      float s = 0.f;
+      for (int i = 0; i < wpr; ++i) s += red[t][mine * wpr + i];
+      r = rsqrtf(s / a.D[t] + a.eps);
     }
-    T* y = static_cast<T*>(a.out[t]) + row * a.out_rs[t];
+    // cos, sin of the four pairs at channel c of a head, times r
+    auto angles = [&](int c, float2 (&w)[4]) {
+      const float4* t4 = reinterpret_cast<const float4*>(tab + (c >> 1));
+      const float4 x = t4[0], y = t4[1];
+      w[0] = make_float2(x.x * r, x.y * r);
+      w[1] = make_float2(x.z * r, x.w * r);
+      w[2] = make_float2(y.x * r, y.y * r);
+      w[3] = make_float2(y.z * r, y.w * r);
+    };
+    float2 w[4];
+    if constexpr (SAME) angles((in_row * 8) % a.dh, w);
+    T* y = static_cast<T*>(a.out[t]) + row * a.out_rs[t] + in_row * 8;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * wpr * 32 + in_row) * 8;
       if (c >= a.D[t]) break;
+      if constexpr (!SAME) angles(c % a.dh, w);
       float v[8];
       ch[t][i].get(v);
       if (gain) {
         float g[8];
-        load8f(gain + c, g);
+        load8f(gain + i * wpr * 256, g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = v[k] * r[t] * g[k];
+        for (int k = 0; k < 8; k += 2) {
+          const float2 n = fmul2(make_float2(v[k], v[k + 1]), make_float2(g[k], g[k + 1]));
+          v[k] = n.x;
+          v[k + 1] = n.y;
+        }
       }
-      const float4* t4 = reinterpret_cast<const float4*>(&cs[mine * half + ((c % a.dh) >> 1)]);
-      const float4 ta = t4[0], tb = t4[1];
-      const float co[4] = {ta.x, ta.z, tb.x, tb.z}, si[4] = {ta.y, ta.w, tb.y, tb.w};
       float o[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        o[2 * k] = v[2 * k] * co[k] - v[2 * k + 1] * si[k];
-        o[2 * k + 1] = v[2 * k] * si[k] + v[2 * k + 1] * co[k];
+        o[2 * k] = v[2 * k] * w[k].x - v[2 * k + 1] * w[k].y;
+        o[2 * k + 1] = v[2 * k] * w[k].y + v[2 * k + 1] * w[k].x;
       }
-      Chunk<T>::store(y + c, o);
+      Chunk<T>::store(y + i * wpr * 256, o);
     }
   }
 }
@@ -371,8 +382,10 @@ template <typename T>
 static wd_status qknorm_rope_axes(const rows::RopeArgs& a, cudaStream_t st) {
   const int D = a.D[1] > a.D[0] ? a.D[1] : a.D[0], wpr = row_warps(D), tokens = rows::WARPS / wpr;
   Trace tr(KC_ROPE, st);
+  const unsigned grid = static_cast<unsigned>((a.rows + tokens - 1) / tokens);
   row_chunks(D, wpr, [&](auto nv) {
-    rows::k_qknorm_rope_axes<T, nv()><<<static_cast<unsigned>((a.rows + tokens - 1) / tokens), rows::THREADS, 0, st>>>(a, wpr);
+    if (wpr * 256 % a.dh == 0) rows::k_qknorm_rope_axes<T, nv(), true><<<grid, rows::THREADS, 0, st>>>(a, wpr);
+    else rows::k_qknorm_rope_axes<T, nv(), false><<<grid, rows::THREADS, 0, st>>>(a, wpr);
   });
   return launch_status("qknorm_rope_axes");
 }
