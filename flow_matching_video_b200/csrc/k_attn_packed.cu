@@ -5,20 +5,23 @@
 // over the keys of i's own sequence (i, j counted from its first row).  Query
 // heads share kv_heads key/value heads in equal groups.
 //
-// The pipeline is that of k_attn_tc.cu: a block owns two query tiles of 128 rows of
-// one sequence and head; warp 0 loads Q and then K_j, V_j by TMA through a ring,
-// warp 1 issues S_t = Q_t K_j^T and O_t += P_t V_j (P from TMEM), and one softmax
-// warp per 32 rows keeps the running maximum and sum, so the tiles' softmaxes and
-// products alternate.  What packing adds:
-//  - blocks find their (sequence, tile) by a scan over cu_q; the grid has the
-//    largest number of tiles that q_rows rows in n_seq sequences can make, and
-//    blocks without a tile leave at once;
-//  - a sequence's last key block runs into the next sequence's rows (the TMA clips
+// The products are those of k_attn_tc.cu: two query tiles of 128 rows of one sequence
+// and head, S_t = Q_t K_j^T in TMEM, one softmax thread per row, O_t += P_t V_j with P
+// from TMEM, the two tiles' softmaxes and products alternating.  Around them:
+//  - Blocks are persistent and take their work one pair of tiles after the other from
+//    the hardware's queue: the grid has one block per possible pair, and a running
+//    block cancels the launch of the next pending one and does its work
+//    (clusterlaunchcontrol).  While one pair ends, the next one's Q, K and V are
+//    already loading, so short key sequences (prompts: four key blocks a pair) do not
+//    wait for a block's start and end each time.
+//  - Warp 0 finds each pair's sequence and tile by a scan over cu_q, with the
+//    sequences of most key blocks first (in groups of 32), so that the last pairs to
+//    run are short; it publishes the pair to the other warps.
+//  - A sequence's last key block runs into the next sequence's rows (the TMA clips
 //    at the end of the buffer only).  Its scores behind the end become -inf before
 //    anything reads them, and its V rows are overwritten with zeros in shared
-//    memory before the product, since 0 * NaN of a neighbour would not be 0;
-//  - the second tile of a block may lie behind the sequence's end: it is left out
-//    of every role.
+//    memory before the product, since 0 * NaN of a neighbour would not be 0.
+//  - The second tile of a pair may lie behind the sequence's end: it is left out.
 // The bias table of the head sits in shared memory in log2 units, its ends
 // repeated 160 times so that no index needs clamping; a block of keys that lies R
 // or further from all of a warp's rows takes the one end value instead.  Where an
@@ -31,18 +34,21 @@ namespace pka {
 constexpr int BQ = 128, BK = 128, NQ = 2;
 constexpr int MAX_RADIUS = 1024, PAD = 160;   // PAD >= 127 + 31 + 1: a tile's reach past +-R
 constexpr float LOG2E = 1.4426950408889634f;
+// Warps: 0 loads, 1 issues MMAs, 2 and 3 only fill their warpgroup, 4-7 and 8-11 are the
+// softmax warps of the tiles.  The first warpgroup hands most of its registers on.
+constexpr int THREADS = 384, REGS_FEW = 120, REGS_MANY = 192;
+static_assert(128 * (REGS_FEW + 2 * REGS_MANY) <= THREADS * 168, "registers of the block at launch");
 
 template <int DH, typename TI>
 struct Cfg {
   static constexpr int Q_BYTES = BQ * DH * 2, KV_BYTES = BK * DH * 2;
   static constexpr int HALVES = DH / 64, HALF_BYTES = 128 * 128;   // 64 columns of 128 rows
   static constexpr int RING = 131072 / KV_BYTES;                   // K/V tiles in flight
-  static constexpr int THREADS = 64 + 128 * NQ;
   static constexpr int BIAS_FLOATS = 2 * (MAX_RADIUS + PAD) + 4;
   static constexpr int Q_OFF = 0, RING_OFF = NQ * Q_BYTES, BIAS_OFF = RING_OFF + RING * KV_BYTES;
   static constexpr int BAR_OFF = BIAS_OFF + BIAS_FLOATS * 4;
   static constexpr int SMEM = 1024 + BAR_OFF + 512;
-  static_assert(BAR_OFF % 8 == 0 && SMEM <= 232448, "shared memory of one block");
+  static_assert(BAR_OFF % 16 == 0 && SMEM <= 232448, "shared memory of one block");
   __host__ __device__ static constexpr int s_col(int t) { return 256 * t; }
   __host__ __device__ static constexpr int o_col(int t) { return 256 * t + 128; }
   static constexpr bool HALF = std::is_same<TI, f16>::value;
@@ -51,7 +57,8 @@ struct Cfg {
 };
 
 enum : unsigned { SITE_Q = 0x501, SITE_KVF = 0x502, SITE_KVE = 0x503, SITE_S = 0x504, SITE_P = 0x505, SITE_O = 0x506,
-                  SITE_TAIL = 0x507, SITE_DRAIN = 0x508 };
+                  SITE_TAIL = 0x507, SITE_DRAIN = 0x508, SITE_WORK = 0x509, SITE_WORKE = 0x50a, SITE_QE = 0x50b,
+                  SITE_NEXT = 0x50c, SITE_TAB = 0x50d };
 
 struct Params {
   const int *cu_q, *cu_k;
@@ -65,11 +72,46 @@ struct Params {
   int64_t o_rs;
 };
 
+// One pair of query tiles, as warp 0 publishes it.
+struct Work {
+  int h, seq_row, l0, lq;   // head; the sequence's first row; the pair's first row in it; its rows
+  int key_row, lk;          // the sequence's first key row; its keys
+  int n_lo, nb;             // key blocks n_lo .. n_lo + nb - 1 (nb = 0: zeros; -1: no more work)
+};
+
 // max that keeps a NaN (a row with a NaN score ends as NaN instead of skipping it)
 __device__ __forceinline__ float max_nan(float a, float b) {
   float o;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(a), "f"(b));
   return o;
+}
+__device__ __forceinline__ float max_nan3(float a, float b, float c) {
+  float o;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(o) : "f"(a), "f"(b), "f"(c));
+  return o;
+}
+
+// Asks for the next pending block of this grid to be cancelled; 16 bytes of answer go to
+// `slot`, signalled on `bar`.
+__device__ __forceinline__ void next_block_ask(void* slot, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(slot)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The cancelled block's index along x, or -1 if none was left.
+__device__ __forceinline__ int next_block_answer(const void* slot) {
+  uint32_t x = 0, got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}\n"
+      : "+r"(x), "=r"(got)
+      : "r"(smem_u32(slot))
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
 }
 
 // Rows [lo, hi) of sequence s, inside the buffer whatever the offsets say.
@@ -77,9 +119,47 @@ __device__ __forceinline__ int2 extent(const int* cu, int s, int rows) {
   const int lo = min(max(cu[s], 0), rows);
   return make_int2(lo, max(min(cu[s + 1], rows), lo));
 }
+// Bias in log2 units; finite values stay finite (they absorb any score either way).
+__device__ __forceinline__ float log2_units(float b) { return isinf(b) ? b : fminf(fmaxf(b * LOG2E, -1e30f), 1e30f); }
+
+// Pair `index` of the grid (whole warp): the sequences with the most key blocks come
+// first (within each group of 32), and the pairs of one sequence run head after head, so
+// that the blocks at work share one head's keys and values in L2.  False: no such pair.
+__device__ __forceinline__ bool find_work(const Params& p, int index, int lane, Work& w) {
+  int left = index;
+  for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
+    const int s = s0 + lane;
+    const bool in = s < p.n_seq;
+    const int2 eq = in ? extent(p.cu_q, s, p.q_rows) : make_int2(0, 0);
+    const int2 ek = in ? extent(p.cu_k, s, p.k_rows) : make_int2(0, 0);
+    const int pairs = (eq.y - eq.x + NQ * BQ - 1) / (NQ * BQ), cost = (ek.y - ek.x + BK - 1) / BK;
+    const int mine = pairs * p.heads;
+    int before = 0;   // pairs of the sequences that come before this lane's
+#pragma unroll 4
+    for (int j = 0; j < 32; ++j) {
+      const int pj = __shfl_sync(0xffffffffu, mine, j), cj = __shfl_sync(0xffffffffu, cost, j);
+      if (cj > cost || (cj == cost && j < lane)) before += pj;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, left >= before && left - before < mine);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      w.seq_row = __shfl_sync(0xffffffffu, eq.x, src);
+      w.lq = __shfl_sync(0xffffffffu, eq.y, src) - w.seq_row;
+      w.key_row = __shfl_sync(0xffffffffu, ek.x, src);
+      w.lk = __shfl_sync(0xffffffffu, ek.y, src) - w.key_row;
+      left -= __shfl_sync(0xffffffffu, before, src);
+      const int per_head = __shfl_sync(0xffffffffu, pairs, src);
+      w.h = left / per_head;
+      w.l0 = (left - w.h * per_head) * NQ * BQ;
+      return true;
+    }
+    left -= __reduce_add_sync(0xffffffffu, mine);
+  }
+  return false;
+}
 
 template <int DH, typename TI, bool BIAS>
-__global__ void __launch_bounds__(Cfg<DH, TI>::THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
 k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   using C = Cfg<DH, TI>;
@@ -87,307 +167,397 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* tab = reinterpret_cast<float*>(smem + C::BIAS_OFF);   // tab[d + R + PAD] = bias at distance d
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-  uint64_t* q_full = bars;
-  uint64_t* tail = bars + 1;              // the last V tile has landed (before its rows are cleared)
-  uint64_t* kv_full = bars + 2;           // RING
+  uint8_t* answer = smem + C::BAR_OFF;                          // 16 bytes: the queue's answer
+  Work* work = reinterpret_cast<Work*>(answer + 16);            // [2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(work + 2);
+  uint64_t* asked = bars;
+  uint64_t* tail = bars + 1;              // a last V tile has landed (before its rows are cleared)
+  uint64_t* work_full = bars + 2;         // [2]
+  uint64_t* work_empty = bars + 4;        // [2]
+  uint64_t* q_full = bars + 6;            // NQ
+  uint64_t* q_empty = q_full + NQ;        // NQ
+  uint64_t* kv_full = q_empty + NQ;       // RING
   uint64_t* kv_empty = kv_full + RING;    // RING
   uint64_t* s_full = kv_empty + RING;     // NQ
   uint64_t* p_part = s_full + NQ;         // NQ: the first 64 keys of P written
   uint64_t* p_full = p_part + NQ;         // NQ: all of P written
   uint64_t* o_done = p_full + NQ;         // NQ
-  uint64_t* tdone = o_done + NQ;
+  uint64_t* tab_bar = o_done + NQ;        // the softmax warps around a change of the bias table
+  uint64_t* tdone = tab_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdone + 1);
+  static_assert(16 + 2 * sizeof(Work) + (6 + 2 * NQ + 2 * RING + 4 * NQ + 3) * 8 <= 512, "barrier space");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
-
-  // ---------------------------------------------------------- which sequence and tile
-  int seq = -1, l0 = 0;
-  int2 eq = make_int2(0, 0);
-  for (int s0 = 0, left = blockIdx.x; s0 < p.n_seq; s0 += 32) {
-    const int s = s0 + lane;
-    const int2 e = s < p.n_seq ? extent(p.cu_q, s, p.q_rows) : make_int2(0, 0);
-    const int mine = (e.y - e.x + NQ * BQ - 1) / (NQ * BQ);
-    int upto = mine;   // tiles of sequences s0 .. s
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, upto > left);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      seq = s0 + src;
-      eq.x = __shfl_sync(0xffffffffu, e.x, src);
-      eq.y = __shfl_sync(0xffffffffu, e.y, src);
-      l0 = (left - __shfl_sync(0xffffffffu, upto - mine, src)) * NQ * BQ;
-      break;
-    }
-    left -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  if (seq < 0) return;
-  const int2 ek = extent(p.cu_k, seq, p.k_rows);
-  const int lq = eq.y - eq.x, lk = ek.y - ek.x;
-  const int nt = lq - l0 > BQ ? 2 : 1;                     // tiles with rows
-  const int l1 = min(l0 + NQ * BQ, lq);
-  // key blocks [n_lo, n_hi): all, or those that some row sees when an end of the table is -inf
-  int n_lo = 0, n_hi = (lk + BK - 1) / BK;
-  float far_lo = 0.f, far_hi = 0.f;                        // the ends of the table, log2 units
-  const int R = p.radius;
-  auto log2_units = [](float b) {   // finite values kept finite: they absorb any score either way
-    return isinf(b) ? b : fminf(fmaxf(b * LOG2E, -1e30f), 1e30f);
-  };
-  if constexpr (BIAS) {
-    const float* tb = p.bias + static_cast<int64_t>(h) * (2 * R + 1);
-    far_lo = log2_units(tb[0]);
-    far_hi = log2_units(tb[2 * R]);
-    if (far_lo == -INFINITY) n_lo = max(0, l0 - R + 1) / BK;
-    if (far_hi == -INFINITY) n_hi = min(n_hi, (l1 - 1 + R - 1) / BK + 1);
-    for (int i = threadIdx.x; i < 2 * (R + PAD) + 1; i += C::THREADS)
-      tab[i] = log2_units(tb[min(max(i - PAD, 0), 2 * R)]);
-  }
-  const int NB = n_hi - n_lo;
-  if (NB <= 0) {   // no row of these tiles sees a key: zeros
-    for (int i = threadIdx.x; i < (l1 - l0) * (DH / 8); i += C::THREADS) {
-      const int64_t row = eq.x + l0 + i / (DH / 8);
-      reinterpret_cast<uint4*>(p.o + row * p.o_rs + h * DH)[i % (DH / 8)] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    return;
-  }
-
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
+    mbar_init(asked, 1);
     mbar_init(tail, 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&work_full[i], 1); mbar_init(&work_empty[i], 1 + 4 * NQ); }
     for (int s = 0; s < RING; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
     for (int t = 0; t < NQ; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
       mbar_init(&p_part[t], 4);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_done[t], 1);
     }
+    mbar_init(tab_bar, 4 * NQ);
     mbar_init(tdone, 1);
     fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int R = p.radius;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA loader
-    const int kvc = h / p.group * DH;
-    const int rest = lk - (n_hi - 1) * BK;   // keys of the last block that are the sequence's
-    uint32_t issued = 0, last_par = 0;
-    bool ok = true;
-    auto load = [&](int i, const CUtensorMap* tm, int row, uint64_t* bar) {   // ring position i
-      uint8_t* dst = smem + C::RING_OFF + (i % RING) * C::KV_BYTES;
-      mbar_arrive_expect_tx(bar, C::KV_BYTES);
-      for (int hf = 0; hf < C::HALVES; ++hf) tma_load_3d(dst + hf * C::HALF_BYTES, tm, kvc + hf * 64, row, 0, bar);
-    };
-    auto ring = [&](int i, const CUtensorMap* tm, int row) -> bool {
-      const int slot = i % RING;
-      const uint32_t ph = (i / RING) & 1u;
-      if (!mbar_wait(&kv_empty[slot], ph ^ 1u, SITE_KVE)) return false;
-      load(i, tm, row, &kv_full[slot]);
-      issued |= 1u << slot;
-      last_par = (last_par & ~(1u << slot)) | (ph << slot);
-      return true;
-    };
-    const bool clear = rest < BK;
-    const int last = 2 * NB - 1;             // ring position of the last V tile
-    if (lane == 0) {
-      mbar_arrive_expect_tx(q_full, nt * C::Q_BYTES);
-      for (int t = 0; t < nt; ++t)
-        for (int hf = 0; hf < C::HALVES; ++hf)
-          tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + hf * C::HALF_BYTES, &tmQ, h * DH + hf * 64, eq.x + l0 + t * BQ,
-                      0, q_full);
-      for (int i = 0; i < (clear ? last : last + 1) && ok; ++i)
-        ok = ring(i, (i & 1) ? &tmV : &tmK, ek.x + (n_lo + (i >> 1)) * BK);
-      if (clear && ok) {   // the last V tile lands on its own barrier
-        ok = mbar_wait(&kv_empty[last % RING], ((last / RING) & 1u) ^ 1u, SITE_KVE);
-        if (ok) load(last, &tmV, ek.x + (n_hi - 1) * BK, tail);
-        issued &= ~(1u << (last % RING));   // what that slot held before has been used; `tail` is waited for below
-      }
-    }
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (clear && ok) {
-      // rows [rest, 128) of it to zero: a row is the same 128 bytes of each half in any swizzle
-      ok = mbar_wait_warp(tail, 0, SITE_TAIL);
-      uint8_t* dst = smem + C::RING_OFF + (last % RING) * C::KV_BYTES;
-      for (int hf = 0; hf < C::HALVES; ++hf)
-        for (int i = rest * 8 + lane; i < BK * 8; i += 32)
-          reinterpret_cast<uint4*>(dst + hf * C::HALF_BYTES)[i] = make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(&kv_full[last % RING]);
-    }
-    if (lane == 0) {
-      mbar_wait(q_full, 0, SITE_DRAIN);
-      for (int s = 0; s < RING; ++s)
-        if (issued & (1u << s)) mbar_wait(&kv_full[s], (last_par >> s) & 1u, SITE_DRAIN);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = mbar_wait(q_full, 0, SITE_Q);
-      tc_fence_after();
-      // descriptors as fixed high halves and low halves that step by 16-byte units
-      const uint32_t r0 = smem_u32(smem + C::RING_OFF);
-      const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::Q_OFF), 16, 1024), dk0 = sdesc_sw128(r0, 16, 1024);
-      const uint64_t dv0 = sdesc_sw128(r0, C::HALF_BYTES, 1024);
-      const uint32_t q_lo = static_cast<uint32_t>(dq0), k_lo = static_cast<uint32_t>(dk0), v_lo = static_cast<uint32_t>(dv0);
-      const uint32_t s_hi = static_cast<uint32_t>(dq0 >> 32), v_hi = static_cast<uint32_t>(dv0 >> 32);
-      auto issue_s = [&](int t, int n) {
-        const uint32_t kb = k_lo + ((2 * n) % RING) * (C::KV_BYTES >> 4), qa = q_lo + t * (C::Q_BYTES >> 4);
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * C::HALF_BYTES + (kk & 3) * 32) >> 4;
-          umma_ss_lh(tmem + C::s_col(t), qa + off, s_hi, kb + off, s_hi, C::IDESC_S, kk ? 1u : 0u);
-        }
-        umma_commit(&s_full[t]);
-      };
-      auto issue_pv = [&](int t, int n) -> bool {
-        const int i = 2 * n + 1, slot = i % RING;
-        const uint32_t vb = v_lo + slot * (C::KV_BYTES >> 4);
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (!mbar_wait(part ? &p_full[t] : &p_part[t], n & 1u, SITE_P)) return false;
-          if (part == 0 && t == 0 && !mbar_wait(&kv_full[slot], (i / RING) & 1u, SITE_KVF)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = part * 4; kk < part * 4 + 4; ++kk)
-            umma_ts_lh(tmem + C::o_col(t), tmem + C::s_col(t) + kk * 8, vb + kk * (2048 >> 4), v_hi, C::IDESC_O,
-                       (n | kk) ? 1u : 0u);
-        }
-        if (t == nt - 1) umma_commit(&kv_empty[slot]);
-        return true;
-      };
-      for (int n = 0; n < NB && ok; ++n) {
-        for (int t = 0; t < nt && ok; ++t) {
-          if (n > 0 && !issue_pv(t, n - 1)) { ok = false; break; }
-          if (t == 0) {
-            ok = mbar_wait(&kv_full[(2 * n) % RING], ((2 * n) / RING) & 1u, SITE_KVF);
-            tc_fence_after();
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FEW));
+    if (warp == 0) {
+      // ------------------------------------------------------------ scheduler and TMA loader
+      uint32_t issued = 0, last_par = 0;      // ring slots: loads in flight
+      uint32_t q_count[NQ] = {0, 0}, tails = 0, round = 0;
+      int pos = 0;                            // ring position
+      bool ok = true;
+      for (int index = blockIdx.x, n = 0; ok && index >= 0; ++round) {
+        Work w;
+        if (find_work(p, index, lane, w)) {
+          const int nt = w.lq - w.l0 > BQ ? 2 : 1, l1 = min(w.l0 + NQ * BQ, w.lq);
+          int n_hi = (w.lk + BK - 1) / BK;
+          w.n_lo = 0;
+          if constexpr (BIAS) {   // key blocks that no row sees, behind an end of -inf
+            const float* tb = p.bias + static_cast<int64_t>(w.h) * (2 * R + 1);
+            if (tb[0] == -INFINITY) w.n_lo = max(0, w.l0 - R + 1) / BK;
+            if (tb[2 * R] == -INFINITY) n_hi = min(n_hi, (l1 - 1 + R - 1) / BK + 1);
           }
-          if (ok) issue_s(t, n);
+          w.nb = max(0, n_hi - w.n_lo);
+          ok = mbar_wait_warp(&work_empty[n & 1], ((n >> 1) & 1) ^ 1u, SITE_WORKE);
+          if (!ok) break;
+          if (lane == 0) {
+            work[n & 1] = w;
+            mbar_arrive(&work_full[n & 1]);
+          }
+          ++n;
+          const int kvc = w.h / p.group * DH;
+          const int rest = w.lk - (n_hi - 1) * BK;   // keys of the last block that are the sequence's
+          const bool clear = rest < BK;
+          const int tiles = 2 * w.nb;                // K and V tiles in turn
+          auto load = [&](const CUtensorMap* tm, int row, uint64_t* bar) {
+            uint8_t* dst = smem + C::RING_OFF + (pos % RING) * C::KV_BYTES;
+            mbar_arrive_expect_tx(bar, C::KV_BYTES);
+            for (int hf = 0; hf < C::HALVES; ++hf) tma_load_3d(dst + hf * C::HALF_BYTES, tm, kvc + hf * 64, row, 0, bar);
+          };
+          if (w.nb && lane == 0) {
+            for (int t = 0; t < nt && ok; ++t) {
+              ok = mbar_wait(&q_empty[t], (q_count[t] & 1u) ^ 1u, SITE_QE);
+              if (!ok) break;
+              ++q_count[t];
+              mbar_arrive_expect_tx(&q_full[t], C::Q_BYTES);
+              for (int hf = 0; hf < C::HALVES; ++hf)
+                tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + hf * C::HALF_BYTES, &tmQ, w.h * DH + hf * 64,
+                            w.seq_row + w.l0 + t * BQ, 0, &q_full[t]);
+            }
+            for (int i = 0; i < tiles && ok; ++i, ++pos) {
+              const int slot = pos % RING;
+              const uint32_t ph = (pos / RING) & 1u;
+              ok = mbar_wait(&kv_empty[slot], ph ^ 1u, SITE_KVE);
+              if (!ok) break;
+              const int row = w.key_row + (w.n_lo + (i >> 1)) * BK;
+              if (clear && i == tiles - 1) {   // the last V tile lands on its own barrier
+                load(&tmV, row, tail);
+                issued &= ~(1u << slot);       // what the slot held before has been used
+                break;
+              }
+              load((i & 1) ? &tmV : &tmK, row, &kv_full[slot]);
+              issued |= 1u << slot;
+              last_par = (last_par & ~(1u << slot)) | (ph << slot);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          pos = __shfl_sync(0xffffffffu, pos, 0);
+          if (w.nb && clear && ok) {
+            // rows [rest, 128) of it to zero: a row is the same 128 bytes of each half in any swizzle
+            ok = mbar_wait_warp(tail, tails & 1u, SITE_TAIL);
+            ++tails;
+            uint8_t* dst = smem + C::RING_OFF + (pos % RING) * C::KV_BYTES;
+            for (int hf = 0; hf < C::HALVES; ++hf)
+              for (int i = rest * 8 + lane; i < BK * 8; i += 32)
+                reinterpret_cast<uint4*>(dst + hf * C::HALF_BYTES)[i] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(&kv_full[pos % RING]);
+            ++pos;
+          }
+          if (!ok) break;
         }
-        if (ok) umma_commit(&kv_empty[(2 * n) % RING]);
+        // the next pending block's work, asked for when this pair's loads are under way
+        if (lane == 0) {
+          mbar_arrive_expect_tx(asked, 16);
+          next_block_ask(answer, asked);
+        }
+        ok = mbar_wait_warp(asked, round & 1u, SITE_NEXT);
+        index = ok ? next_block_answer(answer) : -1;
+        fence_proxy_async_smem();   // read before the next answer is written
+        __syncwarp();
+        if (index < 0 && ok) {      // the end, published like a pair
+          ok = mbar_wait_warp(&work_empty[n & 1], ((n >> 1) & 1) ^ 1u, SITE_WORKE);
+          if (lane == 0 && ok) {
+            work[n & 1].nb = -1;
+            mbar_arrive(&work_full[n & 1]);
+          }
+        }
       }
-      for (int t = 0; t < nt && ok; ++t) {
-        ok = issue_pv(t, NB - 1);
-        if (ok) umma_commit(&o_done[t]);
+      if (lane == 0) {
+        for (int t = 0; t < NQ; ++t)
+          if (q_count[t]) mbar_wait(&q_full[t], (q_count[t] - 1) & 1u, SITE_DRAIN);
+        for (int s = 0; s < RING; ++s)
+          if (issued & (1u << s)) mbar_wait(&kv_full[s], (last_par >> s) & 1u, SITE_DRAIN);
       }
-      umma_commit(tdone);
-      mbar_wait(tdone, 0, SITE_DRAIN);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        bool ok = true;
+        // descriptors as fixed high halves and low halves that step by 16-byte units
+        const uint32_t r0 = smem_u32(smem + C::RING_OFF);
+        const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::Q_OFF), 16, 1024), dk0 = sdesc_sw128(r0, 16, 1024);
+        const uint64_t dv0 = sdesc_sw128(r0, C::HALF_BYTES, 1024);
+        const uint32_t q_lo = static_cast<uint32_t>(dq0), k_lo = static_cast<uint32_t>(dk0), v_lo = static_cast<uint32_t>(dv0);
+        const uint32_t s_hi = static_cast<uint32_t>(dq0 >> 32), v_hi = static_cast<uint32_t>(dv0 >> 32);
+        uint32_t u = 0;                   // key blocks so far: K of block u is ring position 2u, V 2u + 1
+        uint32_t blocks[NQ] = {0, 0};     // key blocks of each tile before this pair
+        uint32_t q_count[NQ] = {0, 0};
+        // one pair with NT live tiles (a compile-time number: the issuing thread runs in step
+        // with the tensor pipe, and what it does between two MMAs is what the pipe waits for)
+        auto pair = [&](auto nt_c, int nb) -> bool {
+          constexpr int NT = decltype(nt_c)::value;
+          auto issue_s = [&](int t, uint32_t kslot) {
+            const uint32_t kb = k_lo + kslot * (C::KV_BYTES >> 4), qa = q_lo + t * (C::Q_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::HALF_BYTES + (kk & 3) * 32) >> 4;
+              umma_ss_lh(tmem + C::s_col(t), qa + off, s_hi, kb + off, s_hi, C::IDESC_S, kk ? 1u : 0u);
+            }
+            umma_commit(&s_full[t]);
+          };
+          auto issue_pv = [&](int t, uint32_t v, int j) -> bool {   // block v, the pair's j-th
+            const uint32_t slot = (2 * v + 1) % RING, vb = v_lo + slot * (C::KV_BYTES >> 4);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              if (!mbar_wait(part ? &p_full[t] : &p_part[t], (blocks[t] + j) & 1u, SITE_P)) return false;
+              if (part == 0 && t == 0 && !mbar_wait(&kv_full[slot], ((2 * v + 1) / RING) & 1u, SITE_KVF)) return false;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = part * 4; kk < part * 4 + 4; ++kk)
+                umma_ts_lh(tmem + C::o_col(t), tmem + C::s_col(t) + kk * 8, vb + kk * (2048 >> 4), v_hi, C::IDESC_O,
+                           (j || kk) ? 1u : 0u);
+            }
+            if (t == NT - 1) umma_commit(&kv_empty[slot]);
+            return true;
+          };
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (!mbar_wait(&q_full[t], q_count[t]++ & 1u, SITE_Q)) return false;
+          for (int j = 0; j < nb; ++j, ++u) {
+            const uint32_t kslot = (2 * u) % RING;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if (j > 0 && !issue_pv(t, u - 1, j - 1)) return false;
+              if (t == 0) {
+                if (!mbar_wait(&kv_full[kslot], ((2 * u) / RING) & 1u, SITE_KVF)) return false;
+                tc_fence_after();
+              }
+              issue_s(t, kslot);
+            }
+            umma_commit(&kv_empty[kslot]);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) umma_commit(&q_empty[t]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (!issue_pv(t, u - 1, nb - 1)) return false;
+            umma_commit(&o_done[t]);
+            blocks[t] += nb;
+          }
+          return true;
+        };
+        for (uint32_t n = 0; ok; ++n) {
+          if (!mbar_wait(&work_full[n & 1], (n >> 1) & 1u, SITE_WORK)) break;
+          const int nb = work[n & 1].nb;
+          const bool two = work[n & 1].lq - work[n & 1].l0 > BQ;
+          mbar_arrive(&work_empty[n & 1]);
+          if (nb < 0) break;
+          if (nb == 0) continue;
+          ok = two ? pair(std::integral_constant<int, 2>(), nb) : pair(std::integral_constant<int, 1>(), nb);
+        }
+        umma_commit(tdone);
+        mbar_wait(tdone, 0, SITE_DRAIN);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_MANY));
     // ------------------------------------------------------------ softmax warps
-    const int t = (warp - 2) >> 2, quarter = warp & 3;
-    const int i_w = l0 + t * BQ + quarter * 32;            // the warp's first row
-    const int i = i_w + lane;
+    const int t = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_addr = tmem + lanes + C::s_col(t), o_addr = tmem + lanes + C::o_col(t);
-    float m = -INFINITY, l = 0.f;
-    bool ok = t < nt;
-    for (int n = 0; n < NB && ok; ++n) {
-      const int j0 = (n_lo + n) * BK;
-      if (!mbar_wait_warp(&s_full[t], n & 1u, SITE_S)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t a[4][32];
+    uint32_t blocks = 0, pairs = 0;   // of this tile so far
+    [[maybe_unused]] int tab_h = -1;
+    [[maybe_unused]] uint32_t tabs = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      // The pair stays published until its output is written: the loop over key blocks keeps
+      // only what it needs of it in registers (the row of scores takes 128 of them).
+      const Work& w = work[n & 1];
+      if (!mbar_wait_warp(&work_full[n & 1], (n >> 1) & 1u, SITE_WORK)) break;
+      const int nb = w.nb;
+      if (nb < 0) break;
+      if (nb == 0) {   // no row of the pair sees a key: zeros
+        const int rows = min(w.lq - w.l0, NQ * BQ);
+        for (int i = threadIdx.x - 128; i < rows * (DH / 8); i += 256) {
+          const int64_t row = static_cast<int64_t>(w.seq_row) + w.l0 + i / (DH / 8);
+          reinterpret_cast<uint4*>(p.o + row * p.o_rs + w.h * DH)[i % (DH / 8)] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      if constexpr (BIAS) {
+        if (nb && w.h != tab_h) {   // all softmax warps take the same pairs, so they change heads together
+          const float* tb = p.bias + static_cast<int64_t>(w.h) * (2 * R + 1);
+          auto all_softmax_warps = [&]() -> bool {   // an mbarrier: a warp that gave up must not leave the others waiting
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tab_bar);
+            return mbar_wait_warp(tab_bar, tabs++ & 1u, SITE_TAB);
+          };
+          if (!all_softmax_warps()) break;           // the old table has been used
+          for (int i = threadIdx.x - 128; i < 2 * (R + PAD) + 1; i += 256) tab[i] = log2_units(tb[min(max(i - PAD, 0), 2 * R)]);
+          if (!all_softmax_warps()) break;
+          tab_h = w.h;
+        }
+      }
+      if (nb == 0 || (t == 1 && w.lq - w.l0 <= BQ)) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&work_empty[n & 1]);
+        continue;
+      }
+      const int keys = w.lk - w.n_lo * BK;                               // from the first key block on
+      [[maybe_unused]] const int far = w.n_lo * BK - (w.l0 + t * BQ + quarter * 32);   // its first key, from the warp's first row
+      float m = -INFINITY, l = 0.f;
+      for (int n = 0; n < nb; ++n) {
+        if (!mbar_wait_warp(&s_full[t], blocks & 1u, SITE_S)) { ok = false; break; }
+        ++blocks;
+        tc_fence_after();
+        uint32_t a[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, a[c]);
-      tmem_wait_ld();
-      if constexpr (BIAS) {   // a = scale * s + bias, log2 units
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-        const bool past = j0 - i_w - 31 >= R, before = j0 + BK - 1 - i_w <= -R;   // warp-uniform
-        const float* tj = tab + (j0 - i + R + PAD);
-        const float cb = past ? far_hi : far_lo;
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, a[c]);
+        tmem_wait_ld();
+        if constexpr (BIAS) {   // a = scale * s + bias, log2 units
+          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+          const int d = far + n * BK;
+          const bool past = d - 31 >= R, before = d + BK - 1 <= -R;   // warp-uniform
+          if (past || before) {
+            const float cb = tab[past ? 2 * (R + PAD) : 0];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float2 b = make_float2(cb, cb);
-            if (!past && !before) b = make_float2(tj[c * 32 + k], tj[c * 32 + k + 1]);
-            const float2 x = ffma2(make_float2(__uint_as_float(a[c][k]), __uint_as_float(a[c][k + 1])), sc2, b);
-            a[c][k] = __float_as_uint(x.x);
-            a[c][k + 1] = __float_as_uint(x.y);
+              for (int k = 0; k < 32; k += 2) {
+                const float2 x = ffma2(make_float2(__uint_as_float(a[c][k]), __uint_as_float(a[c][k + 1])), sc2,
+                                       make_float2(cb, cb));
+                a[c][k] = __float_as_uint(x.x);
+                a[c][k + 1] = __float_as_uint(x.y);
+              }
+          } else {
+            const float* tj = tab + (d - lane + R + PAD);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float2 x = ffma2(make_float2(__uint_as_float(a[c][k]), __uint_as_float(a[c][k + 1])), sc2,
+                                       make_float2(tj[c * 32 + k], tj[c * 32 + k + 1]));
+                a[c][k] = __float_as_uint(x.x);
+                a[c][k + 1] = __float_as_uint(x.y);
+              }
           }
-      }
-      const int valid = lk - j0;
-      if (valid < BK) {   // keys behind the sequence's end
+        }
+        const int valid = keys - n * BK;
+        if (valid < BK) {   // keys behind the sequence's end
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c * 32 + k >= valid) a[c][k] = __float_as_uint(-INFINITY);
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (c * 32 + k >= valid) a[c][k] = __float_as_uint(-INFINITY);
-      }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int k = 0; k < 32; ++k) m4[k & 3] = max_nan(m4[k & 3], __uint_as_float(a[c][k]));
-      float mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
-      if constexpr (!BIAS) mx *= p.scale_log2;
-      if (mx == INFINITY) mx = NAN;   // inf - inf below: the row is NaN, whichever pipe its exponentials take
-      // the reference moves only when the maximum grew by more than the threshold (or is NaN);
-      // P stays below 2^8 and the final 1 / l keeps the result exact
-      const bool grow = !(mx <= m + tca::RESCALE_THRESHOLD);
-      const float alpha = grow ? tca::ex2(m - mx) : 1.f;
-      if (grow) m = mx;
-      if (__any_sync(0xffffffffu, grow) && n > 0) {
-        // P V of the block before has completed: its commit precedes the S waited for
+          for (int k = 0; k < 32; k += 2)
+            m4[(k >> 1) & 3] = max_nan3(m4[(k >> 1) & 3], __uint_as_float(a[c][k]), __uint_as_float(a[c][k + 1]));
+        float mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+        if constexpr (!BIAS) mx *= p.scale_log2;
+        if (mx == INFINITY) mx = NAN;   // inf - inf below: the row is NaN, whichever pipe its exponentials take
+        // the reference moves only when the maximum grew by more than the threshold (or is NaN);
+        // P stays below 2^8 and the final 1 / l keeps the result exact
+        const bool grow = !(mx <= m + tca::RESCALE_THRESHOLD);
+        const float alpha = grow ? tca::ex2(m - mx) : 1.f;
+        if (grow) m = mx;
+        if (__any_sync(0xffffffffu, grow) && n > 0) {
+          // P V of the block before has completed: its commit precedes the S waited for
 #pragma unroll 1
-        for (int c = 0; c < DH / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + c * 32, o);
-          tmem_wait_ld();
+          for (int c = 0; c < DH / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c * 32, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st32(o_addr + c * 32, o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(o_addr + c * 32, o);
+          }
+          tmem_wait_st();
+        }
+        // a row that has seen nothing yet has no reference: its exponentials are those of -inf - 0
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 nm2 = make_float2(-ref, -ref), sc2 = make_float2(p.scale_log2, p.scale_log2);
+        float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {   // 16 keys: two in eight exponentials on the FMA pipe (k_attn_tc.cu)
+          uint32_t pk[8];
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const float2 s2 = make_float2(__uint_as_float(a[c >> 1][(c & 1) * 16 + k]),
+                                          __uint_as_float(a[c >> 1][(c & 1) * 16 + k + 1]));
+            const float2 arg = BIAS ? fadd2(s2, nm2) : ffma2(s2, sc2, nm2);
+            const float2 e = (k & 7) == 6 ? tca::exp2_fma2(arg) : make_float2(tca::ex2(arg.x), tca::ex2(arg.y));
+            rs[(k >> 1) & 3] = fadd2(rs[(k >> 1) & 3], e);
+            pk[k >> 1] = C::HALF ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+          }
+          tmem_st8(s_addr + c * 8, pk);
+          if (c == 3) {   // the first 64 keys' product can start
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_part[t]);
+          }
         }
         tmem_wait_st();
+        const float2 r2 = fadd2(fadd2(rs[0], rs[1]), fadd2(rs[2], rs[3]));
+        l = l * alpha + (r2.x + r2.y);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
       }
-      // a row that has seen nothing yet has no reference: its exponentials are those of -inf - 0
-      const float ref = m == -INFINITY ? 0.f : m;
-      const float2 nm2 = make_float2(-ref, -ref), sc2 = make_float2(p.scale_log2, p.scale_log2);
-      float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {   // 16 keys: two in eight exponentials on the FMA pipe (k_attn_tc.cu)
-        uint32_t pk[8];
-#pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const float2 s2 = make_float2(__uint_as_float(a[c >> 1][(c & 1) * 16 + k]),
-                                        __uint_as_float(a[c >> 1][(c & 1) * 16 + k + 1]));
-          const float2 arg = BIAS ? fadd2(s2, nm2) : ffma2(s2, sc2, nm2);
-          const float2 e = (k & 7) == 6 ? tca::exp2_fma2(arg) : make_float2(tca::ex2(arg.x), tca::ex2(arg.y));
-          rs[(k >> 1) & 3] = fadd2(rs[(k >> 1) & 3], e);
-          pk[k >> 1] = C::HALF ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
-        }
-        tmem_st8(s_addr + c * 8, pk);
-        if (c == 3) {   // the first 64 keys' product can start
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_part[t]);
-        }
-      }
-      tmem_wait_st();
-      const float2 r2 = fadd2(fadd2(rs[0], rs[1]), fadd2(rs[2], rs[3]));
-      l = l * alpha + (r2.x + r2.y);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
-    }
-    // ---------------------------------------------------------- output
-    if (ok && mbar_wait_warp(&o_done[t], 0, SITE_O)) {
+      // -------------------------------------------------------- output
+      // (the next pair's S may already be computed meanwhile; its P V waits for this warp's P)
+      if (!ok || !mbar_wait_warp(&o_done[t], pairs & 1u, SITE_O)) { ok = false; break; }
+      ++pairs;
       tc_fence_after();
       const bool dead = m == -INFINITY;   // every score -inf: the row sees nothing
       const float inv = 1.f / l;
-      bf16* dst = p.o + (static_cast<int64_t>(eq.x) + i) * p.o_rs + h * DH;
+      const int i = w.l0 + t * BQ + quarter * 32 + lane, lq = w.lq;
+      bf16* dst = p.o + (static_cast<int64_t>(w.seq_row) + i) * p.o_rs + w.h * DH;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&work_empty[n & 1]);
 #pragma unroll 1
       for (int c = 0; c < DH / 32; ++c) {
         uint32_t o[32];
@@ -403,7 +573,9 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             d4[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
                                pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
         }
+        __syncwarp();
       }
+      tc_fence_before();
     }
   }
 
@@ -427,10 +599,11 @@ static wd_status launch_attn_packed(const CUtensorMap& tq, const CUtensorMap& tk
                                     const pka::Params& p, cudaStream_t st) {
   using C = pka::Cfg<DH, TI>;
   WD_TRY((allow_smem<pka::k_attn_packed<DH, TI, BIAS>>(C::SMEM)));
-  const int64_t slots = p.q_rows / (pka::NQ * pka::BQ) + static_cast<int64_t>(p.n_seq);
-  dim3 grid(static_cast<unsigned>(slots), p.heads);
+  // as many pairs of tiles as q_rows rows in n_seq sequences can make, times heads
+  const int64_t pairs = (p.q_rows / (pka::NQ * pka::BQ) + static_cast<int64_t>(p.n_seq)) * p.heads;
+  if (pairs > 0x7fffffff) { set_error("attention_packed: %lld tiles", (long long)pairs); return WD_ERR_SHAPE; }
   Trace tr(KC_ATTN_SELF, st);
-  pka::k_attn_packed<DH, TI, BIAS><<<grid, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p);
+  pka::k_attn_packed<DH, TI, BIAS><<<static_cast<unsigned>(pairs), pka::THREADS, C::SMEM, st>>>(tq, tk, tv, p);
   return launch_status("attention_packed");
 }
 
