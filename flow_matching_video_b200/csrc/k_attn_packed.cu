@@ -39,14 +39,16 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr int THREADS = 384, REGS_FEW = 120, REGS_MANY = 192;
 static_assert(128 * (REGS_FEW + 2 * REGS_MANY) <= THREADS * 168, "registers of the block at launch");
 
-template <int DH, typename TI>
+template <int DH, typename TI, bool BIAS>
 struct Cfg {
   static constexpr int Q_BYTES = BQ * DH * 2, KV_BYTES = BK * DH * 2;
   static constexpr int HALVES = DH / 64, HALF_BYTES = 128 * 128;   // 64 columns of 128 rows
   static constexpr int RING = 131072 / KV_BYTES;                   // K/V tiles in flight
-  static constexpr int BIAS_FLOATS = 2 * (MAX_RADIUS + PAD) + 4;
-  static constexpr int Q_OFF = 0, RING_OFF = NQ * Q_BYTES, BIAS_OFF = RING_OFF + RING * KV_BYTES;
-  static constexpr int BAR_OFF = BIAS_OFF + BIAS_FLOATS * 4;
+  static constexpr int BIAS_BYTES = BIAS ? (2 * (MAX_RADIUS + PAD) + 4) * 4 : 0;
+  // output staging of a softmax warp: 32 rows x OC columns (64, or 32 where the bias table leaves no room)
+  static constexpr int OC = DH == 128 && BIAS ? 32 : 64, STG_BYTES = 32 * OC * 2;
+  static constexpr int Q_OFF = 0, RING_OFF = NQ * Q_BYTES, STG_OFF = RING_OFF + RING * KV_BYTES;
+  static constexpr int BIAS_OFF = STG_OFF + 4 * NQ * STG_BYTES, BAR_OFF = BIAS_OFF + BIAS_BYTES;
   static constexpr int SMEM = 1024 + BAR_OFF + 512;
   static_assert(BAR_OFF % 16 == 0 && SMEM <= 232448, "shared memory of one block");
   __host__ __device__ static constexpr int s_col(int t) { return 256 * t; }
@@ -162,7 +164,7 @@ template <int DH, typename TI, bool BIAS>
 __global__ void __launch_bounds__(THREADS, 1)
 k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
-  using C = Cfg<DH, TI>;
+  using C = Cfg<DH, TI, BIAS>;
   constexpr int RING = C::RING;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -554,24 +556,39 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       tc_fence_after();
       const bool dead = m == -INFINITY;   // every score -inf: the row sees nothing
       const float inv = 1.f / l;
-      const int i = w.l0 + t * BQ + quarter * 32 + lane, lq = w.lq;
-      bf16* dst = p.o + (static_cast<int64_t>(w.seq_row) + i) * p.o_rs + w.h * DH;
+      // Through shared memory, so that a store writes whole row pieces: a thread holds one row,
+      // and 16 bytes of 32 rows a store would occupy L1 for 32 lines each.  Row r's 16-byte chunk
+      // j lies at chunk j ^ (r mod 8) (or j ^ (r / 2 mod 4) of 64-byte rows): no bank conflicts.
+      const int row0 = w.l0 + t * BQ + quarter * 32, rows = w.lq - row0;   // the warp's first row, rows left
+      bf16* dst = p.o + (static_cast<int64_t>(w.seq_row) + row0) * p.o_rs + w.h * DH;
       __syncwarp();
       if (lane == 0) mbar_arrive(&work_empty[n & 1]);
+      constexpr int CPR = C::OC / 8, RPS = 32 / CPR;   // chunks per row, rows per store
+      uint8_t* stg = smem + C::STG_OFF + (warp - 4) * C::STG_BYTES;
+      auto chunk = [&](int r, int j) -> uint4* {
+        return reinterpret_cast<uint4*>(stg) + r * CPR + (CPR == 8 ? j ^ (r & 7) : j ^ ((r >> 1) & 3));
+      };
 #pragma unroll 1
-      for (int c = 0; c < DH / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(o_addr + c * 32, o);
-        tmem_wait_ld();
-        float v[32];
+      for (int c = 0; c < DH; c += C::OC) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = dead ? 0.f : __uint_as_float(o[k]) * inv;
-        if (i < lq) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
+        for (int c2 = 0; c2 < C::OC; c2 += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c + c2, o);
+          tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = dead ? 0.f : __uint_as_float(o[k]) * inv;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            d4[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                               pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+            *chunk(lane, c2 / 8 + j) =
+                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < CPR; ++k) {
+          const int r = k * RPS + lane / CPR, j = lane % CPR;
+          if (r < rows) *reinterpret_cast<uint4*>(dst + r * p.o_rs + c + 8 * j) = *chunk(r, j);
         }
         __syncwarp();
       }
@@ -597,7 +614,7 @@ static wd_status make_tmap_rows(CUtensorMap* m, CUtensorMapDataType type, const 
 template <int DH, typename TI, bool BIAS>
 static wd_status launch_attn_packed(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                     const pka::Params& p, cudaStream_t st) {
-  using C = pka::Cfg<DH, TI>;
+  using C = pka::Cfg<DH, TI, BIAS>;
   WD_TRY((allow_smem<pka::k_attn_packed<DH, TI, BIAS>>(C::SMEM)));
   // as many pairs of tiles as q_rows rows in n_seq sequences can make, times heads
   const int64_t pairs = (p.q_rows / (pka::NQ * pka::BQ) + static_cast<int64_t>(p.n_seq)) * p.heads;
