@@ -3,7 +3,8 @@
 //   scale[a] (A D_a^T) U_a^T,   D_a [r, K], U_a [N, r],
 // to A W^T + bias before the epilogue.
 //
-// Two kernels.  k_lora_down makes T = scale[a] A D_a^T (fp32 sums, r columns
+// Two kernels, the second launched so that it may start while the first one ends (it
+// waits for T only where its own K loop is over).  k_lora_down makes T = scale[a] A D_a^T (fp32 sums, r columns
 // wide) and k_gemm_lora runs the dense GEMM of k_gemm_tc.cu whose K loop goes on, for
 // each request that meets the row tile, over the r columns of T and U_a: the
 // low-rank product lands in the same TMEM accumulator, so the output is written
@@ -53,11 +54,18 @@ struct Extra {
   const CUtensorMap* tmT;   // slabs [rows, rank], box 64 x 128
   const CUtensorMap* tmU;   // U [n_adapters * N, rank], box 64 x BN
   struct Row { int first, last, act; };
+  // k_lora_down's results from here on
+  __device__ __forceinline__ void wait() const { asm volatile("griddepcontrol.wait;" ::: "memory"); }
   __device__ __forceinline__ Row row(int m) const {
     const int4 t = a.tiles[m];
     return {t.x, t.y, t.z};
   }
   __device__ __forceinline__ int count(const Row& r) const { return r.act * a.parts * ((a.rank + BK - 1) / BK); }
+  // MMAs of the k-th extra block: 16 columns each, none for the zeros behind rank
+  __device__ __forceinline__ int steps(int k) const {
+    const int per = (a.rank + BK - 1) / BK, left = a.rank - k % per * BK;
+    return left >= BK ? BK / 16 : (left + 15) / 16;
+  }
   template <typename F>
   __device__ __forceinline__ void each(const Row& r, int m, int n0, F&& load) const {
     for (int s = r.first, left = r.act; s < r.last && left > 0; ++s) {
@@ -79,28 +87,46 @@ k_gemm_lora(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 }
 
 // ------------------------------------------------------------------ T = scale A D^T
-// One block per slab: 128 rows x rank, K in 64-wide TMA stages, tcgen05 MMAs of
-// 128 x RN x 16 (RN = rank rounded up to 16; the rows of D behind rank belong to the
-// next adapter and their columns are not stored).  Warp 0 loads, warp 1 issues,
-// warps 2-5 take the accumulator out.  Blocks of the first m_tiles also write
-// their row tile's entry of the table.
-constexpr int STAGES = 4, THREADS = 192;
+// One cluster of `split` blocks per slab, each with a share of K: 128 rows x rank, K in
+// 64-wide TMA stages, tcgen05 MMAs of 128 x RN x 16 (RN = rank rounded up to 16; the
+// rows of D behind rank belong to the next adapter and their columns are not stored).
+// Warp 0 loads, warp 1 issues, warps 2-5 take the accumulator out.  The blocks'
+// fp32 parts meet in shared memory across the cluster, summed in a fixed order, each
+// block taking 128 / split of the rows.  The first block of each of the first m_tiles
+// clusters also writes its row tile's entry of the table.
+constexpr int STAGES = 4, THREADS = 192, MAX_SPLIT = 8;
 __host__ __device__ constexpr int stage_bytes(int rn) { return BM * BK * 2 + rn * BK * 2; }
-constexpr int smem_bytes(int rn) { return 1024 + STAGES * stage_bytes(rn) + 256; }
+constexpr int smem_bytes(int rn) { return 1024 + STAGES * stage_bytes(rn); }
+// fp32 parts take the stages' place: rows of rn + 4 floats (no two of 8 neighbouring rows on one bank)
+static_assert(BM * (MAX_RANK + 4) * 4 <= STAGES * stage_bytes(MAX_RANK) && BM * (16 + 4) * 4 <= STAGES * stage_bytes(16),
+              "the parts fit into the stages");
 
 enum : unsigned { SITE_EMPTY = 0x401, SITE_FULL = 0x402, SITE_DONE = 0x403, SITE_DRAIN = 0x404 };
 
-__global__ void __launch_bounds__(THREADS, 1)
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes at shared address `addr` of block `rank` of the cluster
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr, uint32_t rank) {
+  uint32_t peer;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(THREADS)
 k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmD,
-            const __grid_constant__ Args a, int rn, uint32_t tmem_cols, uint32_t idesc) {
+            const __grid_constant__ Args a, int rn, uint32_t tmem_cols, uint32_t idesc, int split) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[STAGES], empty[STAGES], done;
   __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slab = blockIdx.x;
+  const int slab = blockIdx.x / split, part = blockIdx.x % split;
 
-  if (slab < a.m_tiles && threadIdx.x == 0) {
+  if (slab < a.m_tiles && part == 0 && threadIdx.x == 0) {
     // requests [first, last) meet rows [m0, m0 + 128): the first that ends behind m0, up to
     // the first that starts at or behind the tile's end
     const int m0 = slab * BM;
@@ -121,9 +147,10 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     s = lo - 1;
   }
   const int m = slab - s, m0 = m * BM;
-  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, s, m0)) return;   // no such pair: the whole block leaves
+  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, s, m0)) return;   // no such pair: the whole cluster leaves
   const int ad = a.ids[s];
   const int k_iters = (a.K + BK - 1) / BK;
+  const int k0 = k_iters * part / split, kn = k_iters * (part + 1) / split - k0;   // this block's K stages (>= 1)
   const int sb = stage_bytes(rn);
 
   if (threadIdx.x == 0) {
@@ -136,17 +163,19 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  float* mine = reinterpret_cast<float*>(smem);
+  const int ld = rn + 4;
 
   if (warp == 0) {
     if (lane == 0) {
       uint32_t issued = 0, last_par = 0;
-      for (int k = 0; k < k_iters; ++k) {
+      for (int k = 0; k < kn; ++k) {
         const int st = k % STAGES;
         const uint32_t ph = (k / STAGES) & 1u;
         if (!mbar_wait(&empty[st], ph ^ 1u, SITE_EMPTY)) break;
         mbar_arrive_expect_tx(&full[st], sb);
-        tma_load_2d(smem + st * sb, &tmA, k * BK, m0, &full[st]);
-        tma_load_2d(smem + st * sb + BM * BK * 2, &tmD, k * BK, ad * a.rank, &full[st]);
+        tma_load_2d(smem + st * sb, &tmA, (k0 + k) * BK, m0, &full[st]);
+        tma_load_2d(smem + st * sb + BM * BK * 2, &tmD, (k0 + k) * BK, ad * a.rank, &full[st]);
         issued |= 1u << st;
         last_par = (last_par & ~(1u << st)) | (ph << st);
       }
@@ -157,7 +186,7 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t base = smem_u32(smem);
-      for (int k = 0; k < k_iters; ++k) {
+      for (int k = 0; k < kn; ++k) {
         const int st = k % STAGES;
         if (!mbar_wait(&full[st], (k / STAGES) & 1u, SITE_FULL)) break;
         tc_fence_after();
@@ -171,39 +200,53 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       mbar_wait(&done, 0, SITE_DRAIN);
     }
     __syncwarp();
-  } else if (mbar_wait_warp(&done, 0, SITE_DONE)) {
+  } else if (mbar_wait_warp(&done, 0, SITE_DONE)) {   // every stage has been read: the parts may overwrite them
     tc_fence_after();
-    const int q = warp & 3, r = q * 32 + lane, row = m0 + r;
-    const bool mine = row >= seg_lo(a, s) && row < seg_hi(a, s);
-    const float sc = a.scale ? a.scale[ad] : 1.f;
-    bf16* hi = a.slabs + (static_cast<int64_t>(slab) * a.parts * BM + r) * a.rank;
-    bf16* rem = hi + static_cast<int64_t>(BM) * a.rank;
-    for (int c = 0; c < a.rank; c += 32) {
+    const int q = warp & 3, r = q * 32 + lane;
+    for (int c = 0; c < rn; c += 32) {
       uint32_t u[32];
       tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, u);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (c + 8 * j >= a.rank) continue;
-        uint32_t w[4], x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v0 = mine ? sc * __uint_as_float(u[8 * j + 2 * i]) : 0.f;
-          const float v1 = mine ? sc * __uint_as_float(u[8 * j + 2 * i + 1]) : 0.f;
-          w[i] = pack_bf16x2(v0, v1);
-          const float2 f = unpack_bf16x2(w[i]);
-          x[i] = pack_bf16x2(v0 - f.x, v1 - f.y);
-        }
-        *reinterpret_cast<uint4*>(hi + c + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (a.parts == 2) *reinterpret_cast<uint4*>(rem + c + 8 * j) = make_uint4(x[0], x[1], x[2], x[3]);
-      }
+      for (int j = 0; j < 32; j += 4)
+        if (c + j < rn)
+          *reinterpret_cast<float4*>(mine + r * ld + c + j) =
+              make_float4(__uint_as_float(u[j]), __uint_as_float(u[j + 1]), __uint_as_float(u[j + 2]), __uint_as_float(u[j + 3]));
     }
   }
-
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, tmem_cols);
+  // rows [part * 128 / split, ...): all parts' sums, scaled, in bf16
+  const float sc = a.scale ? a.scale[ad] : 1.f;
+  const int rows = BM / split, chunks = a.rank / 8;
+  const int lo = seg_lo(a, s), hi = seg_hi(a, s);
+  for (int i = threadIdx.x; i < rows * chunks; i += THREADS) {
+    const int r = part * rows + i / chunks, c = i % chunks * 8;
+    float v[8] = {};
+    if (m0 + r >= lo && m0 + r < hi) {   // rows of other requests stay zero
+      const uint32_t addr = smem_u32(mine + r * ld + c);
+      for (int p = 0; p < split; ++p) {
+        const float4 x = cluster_ld4(addr, p), y = cluster_ld4(addr + 16, p);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+    }
+    uint32_t w[4], x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v0 = sc * v[2 * j], v1 = sc * v[2 * j + 1];
+      w[j] = pack_bf16x2(v0, v1);
+      const float2 f = unpack_bf16x2(w[j]);
+      x[j] = pack_bf16x2(v0 - f.x, v1 - f.y);
+    }
+    bf16* out = a.slabs + (static_cast<int64_t>(slab) * a.parts * BM + r) * a.rank + c;
+    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (a.parts == 2) *reinterpret_cast<uint4*>(out + static_cast<int64_t>(BM) * a.rank) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  cluster_sync();   // no block leaves while others read its part
 }
 
 }  // namespace lora
@@ -227,8 +270,18 @@ static wd_status launch_lora(const CUtensorMap& ta, const CUtensorMap& tb, const
   if (MODE == EPI_RESID) WD_TRY(make_tmap_f32(&tx, ep.out, a.M, a.N, ep.ldo, 32, 32));
   if (tcg::staged2<MODE>() && (BN / tcg::epi_wg<MODE>()) % 64 == 0)
     WD_TRY(make_tmap_2b(&tx, ep.out, a.M, a.N, ep.ldo, MODE == EPI_STORE_F16));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(tcg::threads<MODE>());
+  cfg.dynamicSmemBytes = C::smem(MODE);
+  cfg.stream = st;
+  cudaLaunchAttribute early{};   // may start before k_lora_down has ended; waits for it in Extra::wait
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
   Trace tr(KC_GEMM, st);
-  lora::k_gemm_lora<BN, MODE><<<grid, tcg::threads<MODE>(), C::smem(MODE), st>>>(ta, tb, tx, tt, tu, ep, a);
+  cudaLaunchKernelEx(&cfg, lora::k_gemm_lora<BN, MODE>, ta, tb, tx, tt, tu, ep, a);
   return launch_status("gemm_lora");
 }
 
@@ -244,6 +297,19 @@ static wd_status dispatch_lora(int mode, const CUtensorMap& ta, const CUtensorMa
   }
   set_error("gemm_lora: bad epilogue %d", mode);
   return WD_ERR_ARG;
+}
+
+// Tile width: the time of a round of tiles goes with the bytes of a K stage, 128 + BN
+// rows, so the width with the least rounds * (128 + BN) is taken.
+static int lora_tile(int m_tiles, int N) {
+  int best = 64;
+  int64_t least = INT64_MAX;
+  for (int bn = 256; bn >= 64; bn /= 2) {
+    if (N % bn) continue;
+    const int64_t tiles = static_cast<int64_t>(m_tiles) * (N / bn), rounds = (tiles + sm_count() - 1) / sm_count();
+    if (rounds * (128 + bn) < least) { least = rounds * (128 + bn); best = bn; }
+  }
+  return best;
 }
 
 static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, const wd_lora& l, int mode, const Epi& ep,
@@ -265,12 +331,26 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   while (cols < static_cast<uint32_t>(rn)) cols *= 2;
   WD_TRY((allow_smem<lora::k_lora_down>(lora::smem_bytes(lora::MAX_RANK))));
   {
+    // enough blocks to fill the SMs a few times over, with 4 stages of K each at least
+    int split = 1;
+    const int k_iters = (K + lora::BK - 1) / lora::BK;
+    while (split < lora::MAX_SPLIT && slabs * split < 4 * sm_count() && k_iters >= 8 * split) split *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(slabs * split));
+    cfg.blockDim = dim3(lora::THREADS);
+    cfg.dynamicSmemBytes = lora::smem_bytes(rn);
+    cfg.stream = st;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = split;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
     Trace tr(KC_GEMM, st);
-    lora::k_lora_down<<<static_cast<unsigned>(slabs), lora::THREADS, lora::smem_bytes(rn), st>>>(
-        ta, td, a, rn, cols, idesc_bf16(lora::BM, rn, 0, 0));
+    cudaLaunchKernelEx(&cfg, lora::k_lora_down, ta, td, a, rn, cols, idesc_bf16(lora::BM, rn, 0, 0), split);
   }
   WD_TRY(launch_status("lora_down"));
-  const int BN = (N % 256 == 0) ? 256 : ((N % 128 == 0) ? 128 : 64);
+  const int BN = lora_tile(a.m_tiles, N);
   WD_TRY(make_tmap_bf16(&tb, W, N, K, K, lora::BK, BN));
   WD_TRY(make_tmap_bf16(&tt, a.slabs, slabs * a.parts * lora::BM, l.rank, l.rank, lora::BK, lora::BM));
   WD_TRY(make_tmap_bf16(&tu, l.up, static_cast<int64_t>(l.n_adapters) * N, l.rank, l.rank, lora::BK, BN));

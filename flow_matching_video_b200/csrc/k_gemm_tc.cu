@@ -146,10 +146,6 @@ __device__ __forceinline__ void epilogue32(const Epi& ep, int64_t m, int n, cons
 // for the plain GEMM; the low-rank products of k_gemm_lora.cu implement these.
 struct NoExtra {
   static constexpr bool ON = false;
-  struct Row {};
-  __device__ __forceinline__ Row row(int) const { return {}; }
-  __device__ __forceinline__ int count(const Row&) const { return 0; }
-  template <typename F> __device__ __forceinline__ void each(const Row&, int, int, F&&) const {}
 };
 
 template <int BN, int MODE, bool F8, typename X>
@@ -208,6 +204,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
         if constexpr (X::ON) {
+          ex.wait();
           if (ok) ex.each(ex.row(t / n_tiles), t / n_tiles, n0, [&](const CUtensorMap* ta, int ac, int ar,
                                                                     const CUtensorMap* tb, int bc, int br) -> bool {
             if (!mbar_wait(&empty[stage], phase ^ 1u, SITE_EMPTY)) return ok = false;
@@ -241,9 +238,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, SITE_TEMPTY)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
-        int iters = k_iters;
-        if constexpr (X::ON) iters += ex.count(ex.row(t / n_tiles));
-        for (int k = 0; k < iters; ++k) {
+        for (int k = 0; k < k_iters; ++k) {
           if (!mbar_wait(&full[stage], phase, SITE_FULL)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_lo = a_lo0 + stage * (C::A_BYTES >> 4), b_lo = b_lo0 + stage * (C::B_BYTES >> 4);
@@ -256,6 +251,20 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           }
           umma_commit(&empty[stage]);   // frees the smem slot once these MMAs have read it
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if constexpr (X::ON) {
+          ex.wait();
+          const int extra = ok ? ex.count(ex.row(t / n_tiles)) : 0;
+          for (int k = 0; k < extra; ++k) {
+            if (!mbar_wait(&full[stage], phase, SITE_FULL)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a_lo = a_lo0 + stage * (C::A_BYTES >> 4), b_lo = b_lo0 + stage * (C::B_BYTES >> 4);
+            const int steps = ex.steps(k);
+            for (int kk = 0; kk < steps; ++kk)
+              umma_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, C::IDESC, 1u);
+            umma_commit(&empty[stage]);
+            if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+          }
         }
         if (!ok) break;
         umma_commit(&tfull[acc]);       // accumulator ready for the epilogue
