@@ -36,15 +36,60 @@ struct Args {
   int M, N, K;
   int m_tiles;
   bf16* slabs;          // [m_tiles + n_seg][parts][128][rank]
-  int4* tiles;          // [m_tiles]: first request, one past the last, active ones
+  int4* tiles;          // [m_tiles]: where the tile's list begins, its length, and its first entry
+  int2* list;           // [m_tiles + n_seg]: (slab, adapter) of each tile's active requests
 };
 
-// Rows [lo, hi) of request s, kept inside the matrix whatever the offsets say.
-__device__ __forceinline__ int seg_lo(const Args& a, int s) { return min(max(a.seg[s], 0), a.M); }
-__device__ __forceinline__ int seg_hi(const Args& a, int s) { return max(min(a.seg[s + 1], a.M), seg_lo(a, s)); }
-__device__ __forceinline__ bool active(const Args& a, int s, int m0) {
-  const int lo = seg_lo(a, s), hi = seg_hi(a, s);
-  return static_cast<unsigned>(a.ids[s]) < static_cast<unsigned>(a.n_adapters) && max(lo, m0) < min(hi, m0 + BM);
+// Rows [x, y) of request s, kept inside the matrix whatever the offsets say.
+__device__ __forceinline__ int2 seg_rows(const Args& a, int s) {
+  const int lo = min(max(a.seg[s], 0), a.M);
+  return make_int2(lo, max(min(a.seg[s + 1], a.M), lo));
+}
+// Whether request s has an adapter and rows in the tile at m0.
+__device__ __forceinline__ bool active(const Args& a, int2 rows, int id, int m0) {
+  return static_cast<unsigned>(id) < static_cast<unsigned>(a.n_adapters) && max(rows.x, m0) < min(rows.y, m0 + BM);
+}
+
+// The last s in [0, n) with ok(s), where ok holds up to some s and not behind it; -1 if
+// nowhere.  A whole warp, 32 places at a time: one round of loads up to 32 requests,
+// two up to 1024.
+template <typename F>
+__device__ __forceinline__ int last_where(int n, int lane, F&& ok) {
+  int lo = 0, hi = n, best = -1;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5, s = lo + lane * step;
+    const unsigned yes = __ballot_sync(0xffffffffu, s < hi && ok(s));
+    if (!yes) break;
+    best = lo + (31 - __clz(yes)) * step;
+    if (step == 1) break;
+    hi = min(hi, best + step);
+    lo = best + 1;
+  }
+  return best;
+}
+
+// The list of row tile m (a whole warp): from the first request that ends behind its
+// first row to the last that starts before its end, those that are active.
+__device__ __forceinline__ void write_list(const Args& a, int m, int lane) {
+  const int m0 = m * BM;
+  const int first = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] <= m0; });
+  const int last = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] < m0 + BM; });
+  const int begin = max(first, 0);
+  int count = 0;
+  int2 head = make_int2(0, 0);
+  for (int s0 = begin; s0 <= last; s0 += 32) {
+    const int s = s0 + lane;
+    const int id = s <= last ? a.ids[s] : -1;
+    const bool act = s <= last && active(a, seg_rows(a, s), id, m0);
+    const unsigned yes = __ballot_sync(0xffffffffu, act);
+    if (act) a.list[m + begin + count + __popc(yes & ((1u << lane) - 1))] = make_int2(m + s, id);
+    if (!count && yes) {
+      const int src = __ffs(yes) - 1;
+      head = make_int2(m + s0 + src, __shfl_sync(0xffffffffu, id, src));
+    }
+    count += __popc(yes);
+  }
+  if (lane == 0) a.tiles[m] = make_int4(m + begin, count, head.x, head.y);
 }
 
 // The extra K-blocks of gemm_body: request after request, part after part.
@@ -53,27 +98,31 @@ struct Extra {
   const Args& a;
   const CUtensorMap* tmT;   // slabs [rows, rank], box 64 x 128
   const CUtensorMap* tmU;   // U [n_adapters * N, rank], box 64 x BN
-  struct Row { int first, last, act; };
+  using Row = int4;
   // k_lora_down's results from here on
   __device__ __forceinline__ void wait() const { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+  // (volatile: issued where it stands, a whole K loop before its first use)
   __device__ __forceinline__ Row row(int m) const {
-    const int4 t = a.tiles[m];
-    return {t.x, t.y, t.z};
+    int4 t;
+    asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(t.x), "=r"(t.y), "=r"(t.z), "=r"(t.w) : "l"(a.tiles + m) : "memory");
+    return t;
   }
-  __device__ __forceinline__ int count(const Row& r) const { return r.act * a.parts * ((a.rank + BK - 1) / BK); }
+  __device__ __forceinline__ int per_part() const { return (a.rank + BK - 1) / BK; }
+  __device__ __forceinline__ int count(const Row& r) const { return r.y * a.parts * per_part(); }
   // MMAs of the k-th extra block: 16 columns each, none for the zeros behind rank
   __device__ __forceinline__ int steps(int k) const {
-    const int per = (a.rank + BK - 1) / BK, left = a.rank - k % per * BK;
+    const int left = a.rank - k % per_part() * BK;
     return left >= BK ? BK / 16 : (left + 15) / 16;
   }
   template <typename F>
-  __device__ __forceinline__ void each(const Row& r, int m, int n0, F&& load) const {
-    for (int s = r.first, left = r.act; s < r.last && left > 0; ++s) {
-      if (!active(a, s, m * BM)) continue;
-      --left;
+  __device__ __forceinline__ void each(const Row& r, int n0, F&& load) const {
+    int2 e = make_int2(r.z, r.w);
+    for (int i = 0; i < r.y; ++i) {
+      const int2 next = i + 1 < r.y ? a.list[r.x + i + 1] : e;   // fetched while this one's loads are issued
       for (int p = 0; p < a.parts; ++p)
         for (int k = 0; k < a.rank; k += BK)
-          if (!load(tmT, k, ((m + s) * a.parts + p) * BM, tmU, k, a.ids[s] * a.N + n0)) return;
+          if (!load(tmT, k, (e.x * a.parts + p) * BM, tmU, k, e.y * a.N + n0)) return;
+      e = next;
     }
   }
 };
@@ -92,9 +141,9 @@ k_gemm_lora(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 // rows of D behind rank belong to the next adapter and their columns are not stored).
 // Warp 0 loads, warp 1 issues, warps 2-5 take the accumulator out.  The blocks'
 // fp32 parts meet in shared memory across the cluster, summed in a fixed order, each
-// block taking 128 / split of the rows.  The first block of each of the first m_tiles
-// clusters also writes its row tile's entry of the table.
-constexpr int STAGES = 4, THREADS = 192, MAX_SPLIT = 8;
+// block taking 128 / split of the rows.  A warp of the first block of each of the first
+// m_tiles clusters also writes its row tile's list.
+constexpr int STAGES = 3, THREADS = 192, MAX_SPLIT = 8;   // three stages: three blocks an SM up to rank 32
 __host__ __device__ constexpr int stage_bytes(int rn) { return BM * BK * 2 + rn * BK * 2; }
 constexpr int smem_bytes(int rn) { return 1024 + STAGES * stage_bytes(rn); }
 // fp32 parts take the stages' place: rows of rn + 4 floats (no two of 8 neighbouring rows on one bank)
@@ -126,29 +175,18 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slab = blockIdx.x / split, part = blockIdx.x % split;
 
-  if (slab < a.m_tiles && part == 0 && threadIdx.x == 0) {
-    // requests [first, last) meet rows [m0, m0 + 128): the first that ends behind m0, up to
-    // the first that starts at or behind the tile's end
-    const int m0 = slab * BM;
-    int lo = 0, hi = a.n_seg;
-    while (lo < hi) { const int mid = (lo + hi) >> 1; if (a.seg[mid + 1] > m0) hi = mid; else lo = mid + 1; }
-    int act = 0, s = lo;
-    for (; s < a.n_seg && a.seg[s] < m0 + BM; ++s) act += active(a, s, m0);
-    a.tiles[slab] = make_int4(lo, s, act, 0);
-  }
+  if (threadIdx.x == 0) { tma_prefetch_desc(&tmA); tma_prefetch_desc(&tmD); }
   // the pair (m, s) of this slab: the last s whose request starts before the end of tile slab - s
-  int s = -1;
-  {
-    int lo = 0, hi = a.n_seg;   // first s that does not
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (a.seg[mid] < (slab - mid + 1) * BM) lo = mid + 1; else hi = mid;
-    }
-    s = lo - 1;
-  }
+  const int s = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] < (slab - s + 1) * BM; });
   const int m = slab - s, m0 = m * BM;
-  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, s, m0)) return;   // no such pair: the whole cluster leaves
-  const int ad = a.ids[s];
+  const bool lists = slab < a.m_tiles && part == 0 && warp == 5;   // this warp also writes tile `slab`'s list
+  int2 rows_s = make_int2(0, 0);
+  int ad = -1;
+  if (s >= 0) { rows_s = seg_rows(a, s); ad = a.ids[s]; }
+  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, rows_s, ad, m0)) {   // no such pair: the whole cluster leaves
+    if (lists) write_list(a, slab, lane);
+    return;
+  }
   const int k_iters = (a.K + BK - 1) / BK;
   const int k0 = k_iters * part / split, kn = k_iters * (part + 1) / split - k0;   // this block's K stages (>= 1)
   const int sb = stage_bytes(rn);
@@ -200,18 +238,21 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       mbar_wait(&done, 0, SITE_DRAIN);
     }
     __syncwarp();
-  } else if (mbar_wait_warp(&done, 0, SITE_DONE)) {   // every stage has been read: the parts may overwrite them
-    tc_fence_after();
-    const int q = warp & 3, r = q * 32 + lane;
-    for (int c = 0; c < rn; c += 32) {
-      uint32_t u[32];
-      tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, u);
-      tmem_wait_ld();
+  } else {
+    if (lists) write_list(a, slab, lane);
+    if (mbar_wait_warp(&done, 0, SITE_DONE)) {   // every stage has been read: the parts may overwrite them
+      tc_fence_after();
+      const int q = warp & 3, r = q * 32 + lane;
+      for (int c = 0; c < rn; c += 32) {
+        uint32_t u[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, u);
+        tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        if (c + j < rn)
-          *reinterpret_cast<float4*>(mine + r * ld + c + j) =
-              make_float4(__uint_as_float(u[j]), __uint_as_float(u[j + 1]), __uint_as_float(u[j + 2]), __uint_as_float(u[j + 3]));
+        for (int j = 0; j < 32; j += 4)
+          if (c + j < rn)
+            *reinterpret_cast<float4*>(mine + r * ld + c + j) =
+                make_float4(__uint_as_float(u[j]), __uint_as_float(u[j + 1]), __uint_as_float(u[j + 2]), __uint_as_float(u[j + 3]));
+      }
     }
   }
   tc_fence_before();
@@ -222,16 +263,22 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   // rows [part * 128 / split, ...): all parts' sums, scaled, in bf16
   const float sc = a.scale ? a.scale[ad] : 1.f;
   const int rows = BM / split, chunks = a.rank / 8;
-  const int lo = seg_lo(a, s), hi = seg_hi(a, s);
   for (int i = threadIdx.x; i < rows * chunks; i += THREADS) {
     const int r = part * rows + i / chunks, c = i % chunks * 8;
     float v[8] = {};
-    if (m0 + r >= lo && m0 + r < hi) {   // rows of other requests stay zero
+    if (m0 + r >= rows_s.x && m0 + r < rows_s.y) {   // rows of other requests stay zero
       const uint32_t addr = smem_u32(mine + r * ld + c);
-      for (int p = 0; p < split; ++p) {
-        const float4 x = cluster_ld4(addr, p), y = cluster_ld4(addr + 16, p);
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      for (int p0 = 0; p0 < split; p0 += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p)   // all on their way before the first is added
+          if (p0 + p < split) { x[p] = cluster_ld4(addr, p0 + p); y[p] = cluster_ld4(addr + 16, p0 + p); }
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          if (p0 + p < split) {
+            v[0] += x[p].x; v[1] += x[p].y; v[2] += x[p].z; v[3] += x[p].w;
+            v[4] += y[p].x; v[5] += y[p].y; v[6] += y[p].z; v[7] += y[p].w;
+          }
       }
     }
     uint32_t w[4], x[4];
@@ -256,7 +303,7 @@ static size_t lora_slab_bytes(int64_t slabs, int rank) { return static_cast<size
 
 size_t gemm_lora_bytes(int M, int n_seg, int rank) {
   const int64_t mt = (static_cast<int64_t>(M) + lora::BM - 1) / lora::BM;
-  return ((lora_slab_bytes(mt + n_seg, rank) + 255) & ~size_t(255)) + static_cast<size_t>(mt) * sizeof(int4);
+  return lora_slab_bytes(mt + n_seg, rank) + static_cast<size_t>(mt) * sizeof(int4) + static_cast<size_t>(mt + n_seg) * sizeof(int2);
 }
 
 template <int BN, int MODE>
@@ -322,7 +369,8 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   a.m_tiles = (M + lora::BM - 1) / lora::BM;
   const int64_t slabs = static_cast<int64_t>(a.m_tiles) + l.n_seg;
   a.slabs = static_cast<bf16*>(ws);
-  a.tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + ((lora_slab_bytes(slabs, l.rank) + 255) & ~size_t(255)));
+  a.tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + lora_slab_bytes(slabs, l.rank));   // a multiple of 4096 bytes on
+  a.list = reinterpret_cast<int2*>(a.tiles + a.m_tiles);
   const int rn = (l.rank + 15) / 16 * 16;
   CUtensorMap ta, tb, td, tt, tu;
   WD_TRY(make_tmap_bf16(&ta, A, M, K, K, lora::BK, lora::BM));
@@ -331,10 +379,10 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   while (cols < static_cast<uint32_t>(rn)) cols *= 2;
   WD_TRY((allow_smem<lora::k_lora_down>(lora::smem_bytes(lora::MAX_RANK))));
   {
-    // enough blocks to fill the SMs a few times over, with 4 stages of K each at least
+    // enough blocks to fill the SMs twice over, with 4 stages of K each at least
     int split = 1;
     const int k_iters = (K + lora::BK - 1) / lora::BK;
-    while (split < lora::MAX_SPLIT && slabs * split < 4 * sm_count() && k_iters >= 8 * split) split *= 2;
+    while (split < lora::MAX_SPLIT && slabs * split < 2 * sm_count() && k_iters >= 8 * split) split *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(slabs * split));
     cfg.blockDim = dim3(lora::THREADS);

@@ -146,6 +146,7 @@ __device__ __forceinline__ void epilogue32(const Epi& ep, int64_t m, int n, cons
 // for the plain GEMM; the low-rank products of k_gemm_lora.cu implement these.
 struct NoExtra {
   static constexpr bool ON = false;
+  using Row = int;
 };
 
 template <int BN, int MODE, bool F8, typename X>
@@ -205,8 +206,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         }
         if constexpr (X::ON) {
           ex.wait();
-          if (ok) ex.each(ex.row(t / n_tiles), t / n_tiles, n0, [&](const CUtensorMap* ta, int ac, int ar,
-                                                                    const CUtensorMap* tb, int bc, int br) -> bool {
+          if (ok) ex.each(ex.row(t / n_tiles), n0, [&](const CUtensorMap* ta, int ac, int ar, const CUtensorMap* tb,
+                                                       int bc, int br) -> bool {
             if (!mbar_wait(&empty[stage], phase ^ 1u, SITE_EMPTY)) return ok = false;
             mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
             tma_load_2d(sA + stage * C::A_BYTES, ta, ac, ar, &full[stage]);
@@ -238,6 +239,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, SITE_TEMPTY)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
+        [[maybe_unused]] typename X::Row row{};
+        if constexpr (X::ON) { if (t != blockIdx.x) row = ex.row(t / n_tiles); }
         for (int k = 0; k < k_iters; ++k) {
           if (!mbar_wait(&full[stage], phase, SITE_FULL)) { ok = false; break; }
           tc_fence_after();
@@ -253,8 +256,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
         if constexpr (X::ON) {
-          ex.wait();
-          const int extra = ok ? ex.count(ex.row(t / n_tiles)) : 0;
+          if (t == blockIdx.x) { ex.wait(); row = ex.row(t / n_tiles); }
+          const int extra = ok ? ex.count(row) : 0;
           for (int k = 0; k < extra; ++k) {
             if (!mbar_wait(&full[stage], phase, SITE_FULL)) { ok = false; break; }
             tc_fence_after();
