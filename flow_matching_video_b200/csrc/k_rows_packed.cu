@@ -12,10 +12,10 @@
 namespace wd {
 namespace rows {
 
-// A row is held by wpr = 1, 2, 4 or 8 warps of a 256-thread block, each lane with NV
-// <= 4 chunks of 8 elements: few registers a thread, so that four blocks share an SM
-// and their loads cover one another's arithmetic.
-constexpr int THREADS = 256, WARPS = THREADS / 32;
+// A row is held by wpr = 1 .. 8 warps, each lane with NV <= 4 chunks of 8 elements: few
+// registers a thread, so that several blocks share an SM and their loads cover one
+// another's arithmetic.  A block has as many rows as fit into 8 warps.
+constexpr int THREADS = 256, WARPS = THREADS / 32;   // at most
 constexpr int MAX_NV = 4, ROW_MAX = MAX_NV * 8 * THREADS;   // widest row: 8192
 
 // Waits for the wpr warps of one row (barrier 1 + the row's place in the block).
@@ -109,7 +109,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red, int warp, int w
 // mod 1, is held as a 64-bit fraction (made on the host in extended precision).
 // pos * f mod 2^64 is then the angle in 2^-64 turns, exact but for f's own
 // rounding (|pos| 2^-65 turns), so far positions lose nothing; the quadrant is
-// its two leading bits and only the rest goes to sincospif.
+// its two leading bits.
 constexpr int MAX_PAIRS = 128;   // head width up to 256
 struct RopeArgs {
   const int* pos;                     // [rows, 3]
@@ -118,18 +118,23 @@ struct RopeArgs {
   const float* gain[2];
   int64_t in_rs[2], out_rs[2];
   int D[2];                           // heads * dh of each tensor; 0: not given
+  float inv_D[2];
   int64_t rows;
   int dh, p1, p2;                     // pairs [0, p1) frame, [p1, p2) row, [p2, dh / 2) column
   float eps;
   uint64_t freq[MAX_PAIRS];
 };
 
+// Within an eighth of a turn, |x| <= pi / 4, Taylor's series to x^9 and x^10 leave 1.8e-9
+// (x^11 / 11!) and 1.1e-10 (x^12 / 12!), below the fp32 rounding of the sums.
 __device__ __forceinline__ float2 turn(int pos, uint64_t f) {
   const uint32_t u = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<int64_t>(pos)) * f) >> 32);
   const uint32_t quad = (u + 0x20000000u) >> 30;                       // nearest quarter turn
-  const int rest = static_cast<int>(u - (quad << 30));                 // within an eighth of a turn of it
-  float s, c;
-  sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s, &c);   // rest * 2^-31 half turns
+  const int rest = static_cast<int>(u - (quad << 30));                 // 2^-32 turns
+  const float x = static_cast<float>(rest) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const float y = x * x;
+  const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
   const float a = (quad & 1u) ? -s : c, b = (quad & 1u) ? c : s;
   return (quad & 2u) ? make_float2(-a, -b) : make_float2(a, b);
 }
@@ -138,8 +143,9 @@ __device__ __forceinline__ float2 turn(int pos, uint64_t f) {
 // cosines and sines once into shared memory: dh / 2 of them against heads * dh / 2
 // rotations each in q and k.  The rows' loads are issued first.  With SAME (dh
 // divides wpr * 256) all chunks of a lane lie at one place of their heads: its four
-// cosines and sines are read once, with the row's 1 / rms multiplied in.
-template <typename T, int NV, bool SAME>
+// cosines and sines are read once, with the row's 1 / rms multiplied in.  FULL: every
+// given row has exactly NV chunks a lane, so nothing is compared against its width.
+template <typename T, int NV, bool SAME, bool FULL>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : (NV == 4 ? 3 : 4))
 k_qknorm_rope_axes(const __grid_constant__ RopeArgs a, int wpr) {
   __shared__ __align__(16) float2 cs[WARPS * MAX_PAIRS];   // [token][pair]
@@ -155,7 +161,7 @@ k_qknorm_rope_axes(const __grid_constant__ RopeArgs a, int wpr) {
     const T* x = static_cast<const T*>(a.in[t]) + row * a.in_rs[t] + in_row * 8;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if ((i * wpr * 32 + in_row) * 8 < a.D[t]) ch[t][i].load(x + i * wpr * 256);
+      if (FULL ? a.D[t] > 0 : (i * wpr * 32 + in_row) * 8 < a.D[t]) ch[t][i].load(x + i * wpr * 256);
   }
   float2* tab = cs + mine * half;
   for (int p = in_row; p < half; p += wpr * 32)
@@ -166,7 +172,7 @@ k_qknorm_rope_axes(const __grid_constant__ RopeArgs a, int wpr) {
     float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if ((i * wpr * 32 + in_row) * 8 < a.D[t]) {
+      if (FULL || (i * wpr * 32 + in_row) * 8 < a.D[t]) {
         float v[8];
         ch[t][i].get(v);
 #pragma unroll
@@ -186,7 +192,7 @@ k_qknorm_rope_axes(const __grid_constant__ RopeArgs a, int wpr) {
     if (gain) {
       float s = 0.f;
       for (int i = 0; i < wpr; ++i) s += red[t][mine * wpr + i];
-      r = rsqrtf(s / a.D[t] + a.eps);
+      r = rsqrtf(fmaf(s, a.inv_D[t], a.eps));
     }
     // cos, sin of the four pairs at channel c of a head, times r
     auto angles = [&](int c, float2 (&w)[4]) {
@@ -203,7 +209,7 @@ k_qknorm_rope_axes(const __grid_constant__ RopeArgs a, int wpr) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * wpr * 32 + in_row) * 8;
-      if (c >= a.D[t]) break;
+      if (FULL ? a.D[t] == 0 : c >= a.D[t]) break;
       if constexpr (!SAME) angles(c % a.dh, w);
       float v[8];
       ch[t][i].get(v);
@@ -360,17 +366,27 @@ __global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a, int w
 }  // namespace rows
 
 // ------------------------------------------------------------------ host side
-// Warps a row of D elements takes, with at most MAX_NV chunks a lane.
-static int row_warps(int D) {
+// How rows of D elements are laid out: nv chunks a lane and wpr warps that hold the row
+// exactly, with the fewest warps, or else a power of two of warps that holds it.
+struct RowShape {
+  int wpr, nv;
+  bool exact;
+  int rows() const { return rows::WARPS / wpr; }           // of a block
+  unsigned threads() const { return static_cast<unsigned>(rows() * wpr * 32); }
+  unsigned blocks(int64_t n) const { return static_cast<unsigned>((n + rows() - 1) / rows()); }
+};
+static RowShape row_shape(int D) {
+  for (int nv = rows::MAX_NV; nv > 0; --nv)
+    if (D % (nv * 256) == 0 && D / (nv * 256) <= rows::WARPS) return {D / (nv * 256), nv, true};
   int w = 1;
-  while (w * 32 * rows::MAX_NV * 8 < D) w *= 2;
-  return w;
+  while (w * 256 * rows::MAX_NV < D) w *= 2;
+  return {w, (D + w * 256 - 1) / (w * 256), false};
 }
 
-// f(integral constant NV) for the chunks a lane of wpr warps needs for D elements.
+// f(integral constant nv)
 template <typename F>
-static void row_chunks(int D, int wpr, F&& f) {
-  switch ((D + wpr * 256 - 1) / (wpr * 256)) {
+static void with_chunks(int nv, F&& f) {
+  switch (nv) {
     case 1: f(std::integral_constant<int, 1>()); break;
     case 2: f(std::integral_constant<int, 2>()); break;
     case 3: f(std::integral_constant<int, 3>()); break;
@@ -380,22 +396,24 @@ static void row_chunks(int D, int wpr, F&& f) {
 
 template <typename T>
 static wd_status qknorm_rope_axes(const rows::RopeArgs& a, cudaStream_t st) {
-  const int D = a.D[1] > a.D[0] ? a.D[1] : a.D[0], wpr = row_warps(D), tokens = rows::WARPS / wpr;
+  const RowShape r = row_shape(a.D[1] > a.D[0] ? a.D[1] : a.D[0]);
+  const bool full = r.exact && (a.D[1] == 0 || a.D[1] == a.D[0]);
+  const unsigned grid = r.blocks(a.rows), threads = r.threads();
   Trace tr(KC_ROPE, st);
-  const unsigned grid = static_cast<unsigned>((a.rows + tokens - 1) / tokens);
-  row_chunks(D, wpr, [&](auto nv) {
-    if (wpr * 256 % a.dh == 0) rows::k_qknorm_rope_axes<T, nv(), true><<<grid, rows::THREADS, 0, st>>>(a, wpr);
-    else rows::k_qknorm_rope_axes<T, nv(), false><<<grid, rows::THREADS, 0, st>>>(a, wpr);
+  with_chunks(r.nv, [&](auto nv) {
+    if (r.wpr * 256 % a.dh) rows::k_qknorm_rope_axes<T, nv(), false, false><<<grid, threads, 0, st>>>(a, r.wpr);
+    else if (full) rows::k_qknorm_rope_axes<T, nv(), true, true><<<grid, threads, 0, st>>>(a, r.wpr);
+    else rows::k_qknorm_rope_axes<T, nv(), true, false><<<grid, threads, 0, st>>>(a, r.wpr);
   });
   return launch_status("qknorm_rope_axes");
 }
 
 template <typename TX, typename TY, typename TO>
 static wd_status add_norm_t(const rows::AddNormArgs& a, cudaStream_t st) {
-  const int wpr = row_warps(a.D), rpb = rows::WARPS / wpr;
+  const RowShape r = row_shape(a.D);
   Trace tr(KC_NORM, st);
-  row_chunks(a.D, wpr, [&](auto nv) {
-    rows::k_add_norm<TX, TY, TO, nv()><<<static_cast<unsigned>((a.rows + rpb - 1) / rpb), rows::THREADS, 0, st>>>(a, wpr);
+  with_chunks(r.nv, [&](auto nv) {
+    rows::k_add_norm<TX, TY, TO, nv()><<<r.blocks(a.rows), r.threads(), 0, st>>>(a, r.wpr);
   });
   return launch_status("add_norm");
 }

@@ -102,6 +102,7 @@ wd_status wd_qknorm_rope_axes(int dtype, int64_t rows, int dh, const wd_rope_axe
     const int64_t n = i ? kv_heads : heads;
     if (n <= 0 || n * dh > rows::ROW_MAX) { set_error("qknorm_rope_axes: %lld heads of %d (rows up to %d wide)", (long long)n, dh, rows::ROW_MAX); return WD_ERR_SHAPE; }
     a.D[i] = static_cast<int>(n) * dh;
+    a.inv_D[i] = 1.f / a.D[i];
     WD_TRY(check_stride(i ? "qknorm_rope_axes k" : "qknorm_rope_axes q", a.in_rs[i], a.D[i]));
     WD_TRY(check_stride(i ? "qknorm_rope_axes k_out" : "qknorm_rope_axes q_out", a.out_rs[i], a.D[i]));
     if (a.in[i] == a.out[i] && a.in_rs[i] != a.out_rs[i]) {
