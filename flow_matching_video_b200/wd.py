@@ -175,50 +175,54 @@ def _dims(t, n, name):
 
 def _take(where, t, dtype, shape):
     """A dense tensor of this element type and shape."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: a dense {dtype} tensor {list(shape)} is wanted, not {t.dtype} {list(t.shape)}"
                          f" with strides {list(t.stride())}")
 
 
 def _rows(where, t, dtype, width, rows=None):
     """Row stride of a 2D tensor [rows, width] whose rows are dense."""
-    shape = t.shape
-    if t.dtype != dtype or len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows) or \
-            (width > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not dtype or len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows) or \
+            (strides[1] != 1 and width > 1):
         raise ValueError(f"{where}: {dtype} rows of {width} dense elements are wanted, not {t.dtype} {list(shape)}"
-                         f" with strides {list(t.stride())}")
-    return t.stride(0) if shape[0] > 1 else width
+                         f" with strides {list(strides)}")
+    return strides[0] if shape[0] > 1 else width
 
 
 _torch_types = {}
+_torch = None
 
 
 def _torch_type(where, dtype):
-    """The torch type of a WD_* dtype."""
-    if not _torch_types:
-        import torch
-        _torch_types.update({WD_F32: torch.float32, WD_BF16: torch.bfloat16, WD_F16: torch.float16, WD_E4M3: torch.uint8,
-                             "i32": torch.int32})
-    if dtype not in _torch_types:
-        raise ValueError(f"{where}: dtype {dtype}")
-    return _torch_types[dtype]
+    """The torch type of a WD_* dtype (torch is imported with the first one asked for)."""
+    global _torch
+    if _torch is None:
+        import torch as _torch
+        _torch_types.update({WD_F32: _torch.float32, WD_BF16: _torch.bfloat16, WD_F16: _torch.float16,
+                             WD_E4M3: _torch.uint8, "i32": _torch.int32})
+    try:
+        return _torch_types[dtype]
+    except KeyError:
+        raise ValueError(f"{where}: dtype {dtype}") from None
 
 
 def _launch(where, tensors, stream, call):
     """call(stream handle) on the tensors' own device: its current stream, or the one given."""
-    import torch
-    live = [t.get_device() for t in tensors if t is not None]
-    if live[0] < 0 or live.count(live[0]) != len(live):
-        raise ValueError(f"{where}: tensors on {sorted({str(t.device) for t in tensors if t is not None})}, one CUDA"
-                         " device is wanted")
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            raise ValueError(f"{where}: tensors on {sorted({str(t.device) for t in tensors if t is not None})}, one CUDA"
+                             " device is wanted")
     # the stream's handle without a Stream object: 0.1 us instead of 3
-    st = torch._C._cuda_getCurrentRawStream(live[0]) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == live[0]:
+    st = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if _torch.cuda.current_device() == dev:
         status = call(st)
     else:
-        with torch.cuda.device(live[0]):
+        with _torch.cuda.device(dev):
             status = call(st)
-    _ok(status, where)
+    if status:
+        raise WDError(status, where)
 
 
 def make_dims(d) -> wd_dims:
