@@ -13,7 +13,8 @@
 // A row tile (128 rows) may hold the ends of several requests.  T is therefore
 // stored in slabs, one per (row tile m, request s) that meet, with the rows of
 // other requests zero: the extra K-blocks of a tile then add up to each row's own
-// adapter.  Requests are in row order, so the meeting pairs (m, s) form a
+// adapter (U has to be finite for that; masking the rows in the MMA itself instead,
+// by its vector of disabled lanes, gave wrong rows in some instantiations).  Requests are in row order, so the meeting pairs (m, s) form a
 // monotone chain and m + s numbers the slabs without a table.
 //
 // T enters the second product in bf16, rounded once when the output has 2 bytes
@@ -280,14 +281,15 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             v[4] += y[p].x; v[5] += y[p].y; v[6] += y[p].z; v[7] += y[p].w;
           }
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= sc;
     }
     uint32_t w[4], x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float v0 = sc * v[2 * j], v1 = sc * v[2 * j + 1];
-      w[j] = pack_bf16x2(v0, v1);
+      w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
       const float2 f = unpack_bf16x2(w[j]);
-      x[j] = pack_bf16x2(v0 - f.x, v1 - f.y);
+      x[j] = pack_bf16x2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
     }
     bf16* out = a.slabs + (static_cast<int64_t>(slab) * a.parts * BM + r) * a.rank + c;
     *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);

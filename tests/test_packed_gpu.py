@@ -496,3 +496,239 @@ def test_gemm_lora_without_adapters_is_the_gemm(wd):
     wd.wd_gemm(wd.WD_BF16, 300, 256, 256, A, W, None, wd.EPI_F32, ref)
     wd.wd_check()
     assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("what", ["row", "down", "scale"])
+def test_gemm_lora_nan_stays_in_its_request(wd, what):
+    """Requests that share a 128-row tile: a NaN in one's rows, down-projection or scale does
+    not reach the others' rows."""
+    g = gen(13)
+    M, N, K, r = 300, 128, 128, 24
+    seg, ids = [0, 40, 41, 170, 300], [0, 1, 2, 0]
+    A, W = normal(g, (M, K), torch.bfloat16), normal(g, (N, K), torch.bfloat16, 0.1)
+    down, up = normal(g, (3, r, K), torch.bfloat16, K ** -0.5), normal(g, (3, N, r), torch.bfloat16)
+    scale = torch.ones(3, device="cuda")
+    ws = torch.empty(wd.wd_gemm_lora_bytes(M, 4, r), dtype=torch.uint8, device="cuda").fill_(255)
+    outs = []
+    for bad in (False, True):
+        if bad:
+            if what == "row":
+                A[100, 3] = math.nan
+            else:
+                {"down": down, "scale": scale}[what][2] = math.nan
+        out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        wd.wd_gemm_lora(M, N, K, A, W, None, wd.wd_lora.of(ints(seg), ints(ids), down, up, scale), wd.EPI_STORE, out, ws)
+        wd.wd_check()
+        outs.append(out)
+    hit = torch.zeros(M, dtype=torch.bool, device="cuda")
+    hit[100 if what == "row" else slice(41, 170)] = True
+    assert torch.equal(outs[0][~hit], outs[1][~hit]) and not torch.isfinite(outs[1][hit]).all(1).any()
+
+
+# ------------------------------------------------------------------ together, as a packed batch runs them
+class Batch:
+    """Half a block on a packed batch of videos with adapters of their own: the branch before
+    it added and normed, q|k|v with adapters, QK-norm + rotary positions in place, attention,
+    the output projection with adapters added into the residual stream, and the next norm
+    in 8 bits with the FP8 GEMM on it."""
+
+    def __init__(self, wd, lens, ids, seed, H=2, rank=16, spare=5):
+        self.wd, self.lens, self.ids, self.H, self.rank = wd, lens, ids, H, rank
+        g = gen(seed)
+        D = self.D = H * 128
+        n = self.n = sum(lens) + spare
+        self.X, self.y = normal(g, (n, D)), normal(g, (n, D), torch.bfloat16)
+        self.g1, self.g2 = 1 + normal(g, (D,), std=0.1), 1 + normal(g, (D,), std=0.1)
+        self.Wqkv, self.bqkv = normal(g, (3 * D, D), torch.bfloat16, D ** -0.5), normal(g, (3 * D,), std=0.1)
+        self.Wo, self.bo, self.gate = normal(g, (D, D), torch.bfloat16, D ** -0.5), normal(g, (D,), std=0.1), normal(g, (D,))
+        self.gq, self.gk = 1 + normal(g, (D,), std=0.1), 1 + normal(g, (D,), std=0.1)
+        na = 2
+        self.dq, self.uq = normal(g, (na, rank, D), torch.bfloat16, D ** -0.5), normal(g, (na, 3 * D, rank), torch.bfloat16, 0.1)
+        self.do, self.uo = normal(g, (na, rank, D), torch.bfloat16, D ** -0.5), normal(g, (na, D, rank), torch.bfloat16, 0.1)
+        self.scale = torch.rand(na, generator=g, device="cuda") + 0.5
+        self.pos = torch.randint(0, 60, (n, 3), generator=g, device="cuda").int()
+        self.cu, self.adapter = ints(offsets(lens)), ints(ids)
+        self.W8, self.s8 = torch.empty((256, D), dtype=torch.uint8, device="cuda"), torch.empty(256, device="cuda")
+        wd.wd_quant_rows_e4m3(wd.WD_BF16, 256, D, normal(g, (256, D), torch.bfloat16), self.W8, self.s8)
+        e = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")
+        self.h, self.qkv, self.o, self.res = e(n, D), e(n, 3 * D), e(n, D), e(n, D, t=torch.float32)
+        self.h8, self.hs, self.out = e(n, D, t=torch.uint8), e(n, t=torch.float32), e(n, 256, t=torch.float32)
+        self.ws = torch.empty(wd.wd_gemm_lora_bytes(n, len(ids), rank), dtype=torch.uint8, device="cuda")
+        self.lq = wd.wd_lora.of(self.cu, self.adapter, self.dq, self.uq, self.scale)
+        self.lo = wd.wd_lora.of(self.cu, self.adapter, self.do, self.uo, self.scale)
+        self.axes = wd.wd_rope_axes.of((44, 42, 42))
+
+    def run(self, stream=None):
+        wd, n, D, H = self.wd, self.n, self.D, self.H
+        wd.wd_add_norm(wd.WD_F32, self.X, wd.WD_BF16, self.y, wd.WD_NORM_RMS, self.g1, None, 1e-6, self.res, wd.WD_BF16,
+                       self.h, stream=stream)
+        wd.wd_gemm_lora(n, 3 * D, D, self.h, self.Wqkv, self.bqkv, self.lq, wd.EPI_STORE, self.qkv, self.ws, stream=stream)
+        q, k, v = (self.qkv[:, i * D:(i + 1) * D] for i in range(3))
+        wd.wd_qknorm_rope_axes(wd.WD_BF16, 128, self.axes, self.pos, q, self.gq, q, k, self.gk, k, stream=stream)
+        wd.wd_attention_packed(wd.WD_BF16, H, H, 128, q, k, v, self.cu, self.cu, 128 ** -0.5, self.o, stream=stream)
+        wd.wd_gemm_lora(n, D, D, self.o, self.Wo, self.bo, self.lo, wd.EPI_RESID, self.res, self.ws, gate_a=self.gate,
+                        stream=stream)
+        wd.wd_add_norm(wd.WD_F32, self.res, wd.WD_F32, None, wd.WD_NORM_RMS, self.g2, None, 1e-6, None, wd.WD_E4M3, self.h8,
+                       self.hs, stream=stream)
+        wd.wd_gemm_fp8(n, 256, D, self.h8, self.hs, self.W8, self.s8, None, wd.EPI_F32, self.out, stream=stream)
+        return self.res.clone(), self.out.clone()
+
+    def exact(self):
+        """The same in 64 bits, rounded to bf16 where the operators store bf16."""
+        bf = lambda t: t.float().bfloat16().double()
+        cu, D = offsets(self.lens), self.D
+        s, h, _ = norm64(self.X, self.y, self.g1, None, True, 1e-6)
+        qkv, _ = lora64(bf(h), self.Wqkv, self.bqkv, cu, self.ids, self.dq, self.uq, self.scale, 2)
+        q, k, v = (bf(qkv[:, i * D:(i + 1) * D]) for i in range(3))
+        q, k = (bf(rope64(x, self.pos, gn, 128, (44, 42, 42), 10000.0, (1, 1, 1), 1e-6)[0]) for x, gn in ((q, self.gq), (k, self.gk)))
+        o, _ = attention64(q, k, v, cu, cu, self.H, self.H, 128, 128 ** -0.5)
+        p, _ = lora64(bf(o), self.Wo, self.bo, cu, self.ids, self.do, self.uo, self.scale, 2)
+        return s + self.gate.double() * p
+
+
+BATCH = ([300, 1, 0, 130, 77], [1, 0, 1, -1, 0])
+
+
+def test_packed_half_block(wd):
+    b = Batch(wd, *BATCH, seed=1)
+    res, out = b.run()
+    wd.wd_check()
+    want = b.exact()
+    # the bar of the bf16 path: 2e-2 of the output's RMS
+    assert float((res.double() - want).abs().max() / want.pow(2).mean().sqrt()) <= 2e-2
+    # the FP8 GEMM reads the norm's codes and scales
+    a = b.h8.view(torch.float8_e4m3fn).double() * b.hs.double()[:, None]
+    w = b.W8.view(torch.float8_e4m3fn).double() * b.s8.double()[:, None]
+    assert_within(out, a @ w.t(), 2 * b.D * U * (a.abs() @ w.abs().t()) + 3 * U * (a @ w.t()).abs())
+    _, n, bound = norm64(res, None, b.g2, None, True, 1e-6)
+    assert_within(a, n, 1.01 * bound + (2.0 ** -4 * n.abs() + 2.0 ** -10 * b.hs.double()[:, None]) * (1 + 2.0 ** -10))
+    again, out2 = b.run()
+    assert torch.equal(again, res) and torch.equal(out2, out)       # no order of sums varies
+
+
+def test_packed_half_block_captured_and_replayed(wd):
+    """Captured into a CUDA graph, and replayed on inputs, offsets, adapters and positions
+    that were rewritten in place; two graphs alive at once, each with its own workspace."""
+    a, b = Batch(wd, *BATCH, seed=2), Batch(wd, [9, 200, 150, 149, 0], [0, -1, 1, 0, 0], seed=3)
+    graphs = []
+    for x in (a, b):
+        x.run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = x.run()
+        graphs.append((graph, outs))
+    other = Batch(wd, [150, 208, 1, 100, 49], [0, 1, 1, 0, -1], seed=4)
+    assert other.n == a.n
+    for name in ("X", "y", "cu", "adapter", "pos", "Wqkv", "uq"):
+        getattr(a, name).copy_(getattr(other, name))
+    for name in ("g1", "g2", "bqkv", "Wo", "bo", "gate", "gq", "gk", "dq", "do", "uo", "scale", "W8", "s8"):
+        getattr(other, name).copy_(getattr(a, name))
+    graphs[1][0].replay()
+    graphs[0][0].replay()
+    wd.wd_check()
+    for (_, outs), eager in zip(graphs, (other, b)):
+        for got, want in zip(outs, eager.run()):
+            assert torch.equal(got, want)
+
+
+def test_packed_half_blocks_on_two_streams(wd):
+    bs = [Batch(wd, *BATCH, seed=5), Batch(wd, [508], [1], seed=6)]
+    want = [b.run() for b in bs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in bs]
+    for _ in range(5):
+        got = []
+        for b, s in zip(bs, streams):
+            with torch.cuda.stream(s):
+                got.append(b.run())
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    # a stream handed over by the caller, while another one is current
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    bs[0].run(stream=s)
+    s.synchronize()
+    assert torch.equal(bs[0].res, want[0][0])
+
+
+# ------------------------------------------------------------------ far ends
+def test_attention_packed_thousands_of_sequences(wd):
+    """Sequences of 0 to 3 rows, more than any group of the scan, and the rows behind them."""
+    g = gen(20)
+    lens = torch.randint(0, 4, (3000,), generator=torch.Generator().manual_seed(2)).tolist()
+    cu = offsets(lens)
+    n = cu[-1]
+    q, k, v = (normal(g, (n + 7, 128), torch.bfloat16) for _ in range(3))
+    out = torch.full((n + 7, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    wd.wd_attention_packed(wd.WD_BF16, 2, 2, 64, q, k, v, ints(cu), ints(cu), 0.125, out)
+    wd.wd_check()
+    owner = torch.repeat_interleave(torch.arange(3000), torch.tensor(lens)).cuda()
+    t = torch.einsum("ihd,jhd->hij", q[:n].double().view(n, 2, 64), k[:n].double().view(n, 2, 64)) * 0.125
+    p = torch.softmax(t.masked_fill(owner[None, :, None] != owner[None, None, :], -math.inf), -1)
+    vv = v[:n].double().view(n, 2, 64)
+    want, ab = (torch.einsum("hij,jhd->ihd", p, x).reshape(n, 128) for x in (vv, vv.abs()))
+    assert_within(out[:n], want, attention_bound(want, ab, torch.bfloat16, 3, v))
+    assert (out[n:] == 7.0).all()
+
+
+def test_attention_packed_no_rows_at_all(wd):
+    q = torch.randn((300, 128), device="cuda").bfloat16()
+    out = torch.full_like(q, 7.0)
+    zero, cu = ints([0, 0, 0]), ints([0, 100, 300])
+    wd.wd_attention_packed(wd.WD_BF16, 1, 1, 128, q, q, q, zero, cu, 0.1, out)
+    wd.wd_check()
+    assert (out == 7.0).all()
+    wd.wd_attention_packed(wd.WD_BF16, 1, 1, 128, q, q, q, cu, zero, 0.1, out)
+    wd.wd_check()
+    assert (out == 0).all()
+
+
+def test_many_single_row_requests(wd):
+    run_lora(wd, [1] * 700, [i % 5 - 1 for i in range(700)], 705, 128, 128, 8, 4, wd.EPI_STORE)
+    run_lora(wd, [0, 0, 3, 0, 0, 200, 0], [0, 1, 1, 0, 0, 1, 0], 203, 64, 64, 8, 2, wd.EPI_F32)
+
+
+def test_offsets_past_32_bits(wd):
+    """Buffers of more than 2^32 bytes: the rows at their far ends."""
+    g = gen(21)
+    rows, stride = 1_100_000, 2048                      # 2.25e9 elements
+    big = torch.zeros((rows, stride), dtype=torch.bfloat16, device="cuda")
+    q, k, v = (big[:, i * 256:(i + 1) * 256] for i in range(3))
+    n = 300
+    for t in (q, k, v):
+        t[-n - 10:-10] = normal(g, (n, 256), torch.bfloat16)
+    o = big[:, 1024:1280]
+    cu = ints([rows - n - 10, rows - 10])
+    wd.wd_attention_packed(wd.WD_BF16, 2, 2, 128, q, k, v, cu, cu, 0.1, o)
+    wd.wd_check()
+    want, ab = attention64(*(t[-n - 10:-10] for t in (q, k, v)), [0, n], [0, n], 2, 2, 128, 0.1)
+    assert_within(o[-n - 10:-10], want, attention_bound(want, ab, torch.bfloat16, n, v[-n - 10:-10]))
+    assert (o[-10:] == 0).all() and (o[:1000] == 0).all()
+    pos = torch.randint(0, 100, (rows, 3), generator=g, device="cuda").int()
+    r = big[:, 1280:1536]
+    wd.wd_qknorm_rope_axes(wd.WD_BF16, 128, wd.wd_rope_axes.of((44, 42, 42)), pos, q, None, r)
+    wd.wd_check()
+    want, size = rope64(q[-n:], pos[-n:], None, 128, (44, 42, 42), 10000.0, (1, 1, 1), 1e-6)
+    assert_within(r[-n:], want, 64 * U * size + 2.0 ** -8 * want.abs() + 2.0 ** -25)
+    del big, q, k, v, o, r
+    x = torch.zeros((540_000, 4096), dtype=torch.bfloat16, device="cuda")
+    x[-5:] = normal(g, (5, 4096), torch.bfloat16)
+    out = torch.empty_like(x)
+    wd.wd_add_norm(wd.WD_BF16, x, wd.WD_BF16, None, wd.WD_NORM_RMS, None, None, 1e-6, None, wd.WD_BF16, out)
+    wd.wd_check()
+    _, want, bound = norm64(x[-5:], None, None, None, True, 1e-6)
+    assert_within(out[-5:], want, bound + 2.0 ** -8 * want.abs() * (1 + U))
+    del x, out
+    M, N, K, r = 1_060_000, 2048, 64, 8                  # 2.17e9 outputs
+    A, W = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda"), normal(g, (N, K), torch.bfloat16)
+    A[-200:] = normal(g, (200, K), torch.bfloat16)
+    down, up = normal(g, (2, r, K), torch.bfloat16, 0.1), normal(g, (2, N, r), torch.bfloat16)
+    seg, ids = [0, M - 150, M - 20], [0, 1]
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(wd.wd_gemm_lora_bytes(M, 2, r), dtype=torch.uint8, device="cuda")
+    wd.wd_gemm_lora(M, N, K, A, W, None, wd.wd_lora.of(ints(seg), ints(ids), down, up), wd.EPI_STORE, out, ws)
+    wd.wd_check()
+    v, err = lora64(A[-200:], W, torch.zeros(N, device="cuda"), [0, 50, 180], ids, down, up, None, 1)
+    assert_within(out[-200:], v, err * (1 + 2.0 ** -8) + 2.0 ** -8 * v.abs())
