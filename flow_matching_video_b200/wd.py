@@ -207,8 +207,8 @@ def _torch_type(where, dtype):
         raise ValueError(f"{where}: dtype {dtype}") from None
 
 
-def _launch(where, tensors, stream, call):
-    """call(stream handle) on the tensors' own device: its current stream, or the one given."""
+def _launch(where, tensors, stream, call, *args):
+    """call(*args, stream handle) on the tensors' own device: its current stream, or the one given."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and (dev < 0 or t.get_device() != dev):
@@ -217,10 +217,10 @@ def _launch(where, tensors, stream, call):
     # the stream's handle without a Stream object: 0.1 us instead of 3
     st = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
     if _torch.cuda.current_device() == dev:
-        status = call(st)
+        status = call(*args, st)
     else:
         with _torch.cuda.device(dev):
-            status = call(st)
+            status = call(*args, st)
     if status:
         raise WDError(status, where)
 
@@ -360,21 +360,21 @@ def wd_attention_packed(dtype, heads, kv_heads, dh, q, k, v, cu_q, cu_k, scale, 
     """q, o [q_rows, heads*dh], k, v [k_rows, kv_heads*dh] (row strides may differ, k and v
     share theirs), cu_q, cu_k int32 [n_seq + 1], bias fp32 [heads, 2 radius + 1] or None."""
     f = "wd_attention_packed"
-    td = _torch_type(f, dtype)
+    td, i32 = _torch_type(f, dtype), _torch_types["i32"]
     q_rs, k_rs, v_rs = _rows(f, q, td, heads * dh), _rows(f, k, td, kv_heads * dh), _rows(f, v, td, kv_heads * dh, k.shape[0])
-    o_rs = _rows(f, o, _torch_type(f, WD_BF16), heads * dh, q.shape[0])
+    o_rs = _rows(f, o, _torch_types[WD_BF16], heads * dh, q.shape[0])
     if k_rs != v_rs:
         raise ValueError(f"{f}: row strides {k_rs} of k and {v_rs} of v")
     n_seq = cu_q.numel() - 1
-    _take(f, cu_q, _torch_type(f, "i32"), (n_seq + 1,))
-    _take(f, cu_k, _torch_type(f, "i32"), (n_seq + 1,))
+    _take(f, cu_q, i32, (n_seq + 1,))
+    _take(f, cu_k, i32, (n_seq + 1,))
     radius = 0
     if bias is not None:
         radius = (_dims(bias, 2, "bias")[1] - 1) // 2
-        _take(f, bias, _torch_type(f, WD_F32), (heads, 2 * radius + 1))
-    _launch(f, (q, k, v, cu_q, cu_k, o, bias), stream, lambda st: _lib.wd_attention_packed(
-        dtype, n_seq, heads, kv_heads, dh, _p(q), q_rs, q.shape[0], _p(cu_q), _p(k), _p(v), k_rs, k.shape[0], _p(cu_k),
-        float(scale), _p(bias), radius, _p(o), o_rs, st))
+        _take(f, bias, _torch_types[WD_F32], (heads, 2 * radius + 1))
+    _launch(f, (q, k, v, cu_q, cu_k, o, bias), stream, _lib.wd_attention_packed,
+            dtype, n_seq, heads, kv_heads, dh, _p(q), q_rs, q.shape[0], _p(cu_q), _p(k), _p(v), k_rs, k.shape[0], _p(cu_k),
+            scale, _p(bias), radius, _p(o), o_rs)
 
 
 def wd_qknorm_rope_axes(dtype, dh, axes: wd_rope_axes, pos, q, g_q, q_out, k=None, g_k=None, k_out=None, eps=1e-6,
@@ -382,37 +382,47 @@ def wd_qknorm_rope_axes(dtype, dh, axes: wd_rope_axes, pos, q, g_q, q_out, k=Non
     """q, q_out [rows, heads*dh], k, k_out [rows, kv_heads*dh] or None, pos int32 [rows, 3],
     gains fp32 [row width] or None."""
     f = "wd_qknorm_rope_axes"
-    td = _torch_type(f, dtype)
+    td, f32 = _torch_type(f, dtype), _torch_types[WD_F32]
     rows, wq = _dims(q, 2, "q")
-    wk = 0 if k is None else _dims(k, 2, "k")[1]
-    if wq % dh or wk % dh:
-        raise ValueError(f"{f}: rows of {wq} and {wk} elements with heads of {dh}")
-    strides = [_rows(f, t, td, w, rows) if t is not None else 0 for t, w in ((q, wq), (q_out, wq), (k, wk), (k_out, wk))]
-    if (k is None) != (k_out is None):
-        raise ValueError(f"{f}: k without k_out, or k_out without k")
-    _take(f, pos, _torch_type(f, "i32"), (rows, 3))
-    for g, w in ((g_q, wq), (g_k, wk)):
-        if g is not None:
-            _take(f, g, _torch_type(f, WD_F32), (w,))
-    _launch(f, (q, q_out, pos, k, k_out, g_q, g_k), stream, lambda st: _lib.wd_qknorm_rope_axes(
-        dtype, rows, dh, C.byref(axes), _p(pos), _p(q), strides[0], wq // dh, _p(g_q), _p(q_out), strides[1], _p(k),
-        strides[2], wk // dh, _p(g_k), _p(k_out), strides[3], float(eps), st))
+    q_rs, qo_rs = _rows(f, q, td, wq, rows), _rows(f, q_out, td, wq, rows)
+    wk = k_rs = ko_rs = 0
+    if k is not None:
+        wk = _dims(k, 2, "k")[1]
+        k_rs = _rows(f, k, td, wk, rows)
+        if k_out is not None:
+            ko_rs = _rows(f, k_out, td, wk, rows)
+    if (k is None) != (k_out is None) or dh <= 0 or wq % dh or wk % dh:
+        raise ValueError(f"{f}: rows of {wq} and {wk} elements with heads of {dh}; k and k_out go together")
+    _take(f, pos, _torch_types["i32"], (rows, 3))
+    if g_q is not None:
+        _take(f, g_q, f32, (wq,))
+    if g_k is not None:
+        _take(f, g_k, f32, (wk,))
+    _launch(f, (q, q_out, pos, k, k_out, g_q, g_k), stream, _lib.wd_qknorm_rope_axes,
+            dtype, rows, dh, C.byref(axes), _p(pos), _p(q), q_rs, wq // dh, _p(g_q), _p(q_out), qo_rs, _p(k), k_rs, wk // dh,
+            _p(g_k), _p(k_out), ko_rs, eps)
 
 
 def wd_add_norm(x_dtype, x, y_dtype, y, norm, gain, beta, eps, sum, out_dtype, out, scale=None, stream=None):
     """x, y, sum, out [rows, D] dense (y and sum may be None), gain, beta fp32 [D] or None,
     scale fp32 [rows] for the e4m3 output (out uint8)."""
     f = "wd_add_norm"
-    rows, D = _dims(x, 2, "x")
-    for t, td in ((x, x_dtype), (y, y_dtype), (sum, x_dtype), (out, out_dtype)):
-        if t is not None:
-            _take(f, t, _torch_type(f, td), (rows, D))
-    for t, n in ((gain, D), (beta, D), (scale, rows)):
-        if t is not None:
-            _take(f, t, _torch_type(f, WD_F32), (n,))
-    _launch(f, (x, y, gain, beta, sum, out, scale), stream, lambda st: _lib.wd_add_norm(
-        rows, D, x_dtype, _p(x), y_dtype, _p(y), norm, _p(gain), _p(beta), float(eps), _p(sum), out_dtype, _p(out),
-        _p(scale), st))
+    tx, f32 = _torch_type(f, x_dtype), _torch_types[WD_F32]
+    shape = rows, D = _dims(x, 2, "x")
+    _take(f, x, tx, shape)
+    if y is not None:
+        _take(f, y, _torch_type(f, y_dtype), shape)
+    if sum is not None:
+        _take(f, sum, tx, shape)
+    _take(f, out, _torch_type(f, out_dtype), shape)
+    if gain is not None:
+        _take(f, gain, f32, (D,))
+    if beta is not None:
+        _take(f, beta, f32, (D,))
+    if scale is not None:
+        _take(f, scale, f32, (rows,))
+    _launch(f, (x, y, gain, beta, sum, out, scale), stream, _lib.wd_add_norm,
+            rows, D, x_dtype, _p(x), y_dtype, _p(y), norm, _p(gain), _p(beta), eps, _p(sum), out_dtype, _p(out), _p(scale))
 
 
 def wd_gemm_lora_bytes(M: int, n_seg: int, rank: int) -> int:
@@ -423,19 +433,19 @@ def wd_gemm_lora(M, N, K, A, W, bias, lora: wd_lora, epilogue, out, ws, gate_a=N
     """A [M, K], W [N, K] bf16, bias, gates fp32 [N] or None, lora from wd_lora.of, out
     [M, N] in the epilogue's type, ws at least wd_gemm_lora_bytes bytes."""
     f = "wd_gemm_lora"
-    _take(f, A, _torch_type(f, WD_BF16), (M, K))
-    _take(f, W, _torch_type(f, WD_BF16), (N, K))
-    _take(f, out, _torch_type(f, WD_F32 if epilogue in (EPI_F32, EPI_RESID) else
-                              WD_F16 if epilogue == EPI_STORE_F16 else WD_BF16), (M, N))
+    bf16, f32 = _torch_type(f, WD_BF16), _torch_types[WD_F32]
+    _take(f, A, bf16, (M, K))
+    _take(f, W, bf16, (N, K))
+    _take(f, out, f32 if epilogue in (EPI_F32, EPI_RESID) else _torch_types[WD_F16] if epilogue == EPI_STORE_F16 else bf16,
+          (M, N))
     for t in (bias, gate_a, gate_b):
         if t is not None:
-            _take(f, t, _torch_type(f, WD_F32), (N,))
+            _take(f, t, f32, (N,))
     seg, adapter, down, up, scale = lora.tensors
     if down.shape[2] != K or up.shape[1] != N:
         raise ValueError(f"{f}: adapters of {up.shape[1]} x {down.shape[2]} for a layer of {N} x {K}")
-    _launch(f, (A, W, bias, gate_a, gate_b, out, ws, seg, adapter, down, up, scale), stream, lambda st: _lib.wd_gemm_lora(
-        M, N, K, _p(A), _p(W), _p(bias), C.byref(lora), epilogue, _p(out), _p(gate_a), _p(gate_b), _p(ws),
-        ws.numel() * ws.element_size(), st))
+    _launch(f, (A, W, bias, gate_a, gate_b, out, ws, seg, adapter, down, up, scale), stream, _lib.wd_gemm_lora,
+            M, N, K, _p(A), _p(W), _p(bias), C.byref(lora), epilogue, _p(out), _p(gate_a), _p(gate_b), _p(ws), ws.nbytes)
 
 
 def wd_test_exp2(x, y_fma, y_fma2, y_mufu, y_lib, stream=None):
