@@ -3,9 +3,9 @@
 //   scale[a] (A D_a^T) U_a^T,   D_a [r, K], U_a [N, r],
 // to A W^T + bias before the epilogue.
 //
-// Two kernels, the second launched so that it may start while the first one ends (it
+// Two steps, the second launched so that it may start while the first one ends (it
 // waits for T only where its own K loop is over).  k_lora_down makes T = scale[a] A D_a^T (fp32 sums, r columns
-// wide) and k_gemm_lora runs the dense GEMM of k_gemm_tc.cu whose K loop goes on, for
+// wide) and k_gemm_lora or k_gemm_lora2 runs the dense GEMM of k_gemm_tc.cu whose K loop goes on, for
 // each request that meets the row tile, over the r columns of T and U_a: the
 // low-rank product lands in the same TMEM accumulator, so the output is written
 // once and no epilogue knows of it.
@@ -35,8 +35,8 @@ struct Args {
   const float* scale;   // [n_adapters] or null (1)
   int n_seg, n_adapters, rank, parts;
   int M, N, K;
-  int m_tiles;
-  bf16* slabs;          // [m_tiles + n_seg][parts][128][rank]
+  int m_tiles, tile;    // row tiles and their height: 128 rows, or 256 for SM pairs
+  bf16* slabs;          // [m_tiles + n_seg][parts][tile][rank]
   int4* tiles;          // [m_tiles]: where the tile's list begins, its length, and its first entry
   int2* list;           // [m_tiles + n_seg]: (slab, adapter) of each tile's active requests
 };
@@ -46,9 +46,9 @@ __device__ __forceinline__ int2 seg_rows(const Args& a, int s) {
   const int lo = min(max(a.seg[s], 0), a.M);
   return make_int2(lo, max(min(a.seg[s + 1], a.M), lo));
 }
-// Whether request s has an adapter and rows in the tile at m0.
+// Whether a request has an adapter and rows in the tile at m0.
 __device__ __forceinline__ bool active(const Args& a, int2 rows, int id, int m0) {
-  return static_cast<unsigned>(id) < static_cast<unsigned>(a.n_adapters) && max(rows.x, m0) < min(rows.y, m0 + BM);
+  return static_cast<unsigned>(id) < static_cast<unsigned>(a.n_adapters) && max(rows.x, m0) < min(rows.y, m0 + a.tile);
 }
 
 // The last s in [0, n) with ok(s), where ok holds up to some s and not behind it; -1 if
@@ -72,9 +72,9 @@ __device__ __forceinline__ int last_where(int n, int lane, F&& ok) {
 // The list of row tile m (a whole warp): from the first request that ends behind its
 // first row to the last that starts before its end, those that are active.
 __device__ __forceinline__ void write_list(const Args& a, int m, int lane) {
-  const int m0 = m * BM;
+  const int m0 = m * a.tile;
   const int first = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] <= m0; });
-  const int last = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] < m0 + BM; });
+  const int last = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] < m0 + a.tile; });
   const int begin = max(first, 0);
   int count = 0;
   int2 head = make_int2(0, 0);
@@ -122,7 +122,7 @@ struct Extra {
       const int2 next = i + 1 < r.y ? a.list[r.x + i + 1] : e;   // fetched while this one's loads are issued
       for (int p = 0; p < a.parts; ++p)
         for (int k = 0; k < a.rank; k += BK)
-          if (!load(tmT, k, (e.x * a.parts + p) * BM, tmU, k, e.y * a.N + n0)) return;
+          if (!load(tmT, k, (e.x * a.parts + p) * a.tile, tmU, k, e.y * a.N + n0)) return;
       e = next;
     }
   }
@@ -136,8 +136,153 @@ k_gemm_lora(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   tcg::gemm_body<BN, MODE, false>(tmA, tmB, tmX, ep, a.M, a.N, a.K, Extra{a, &tmT, &tmU});
 }
 
+// ------------------------------------------------------------------ the product on SM pairs
+// The same GEMM with tiles of 256 x 256 for a cluster of two blocks: one MMA of both SMs
+// takes 128 rows of A and half of B's 256 rows from each, so a K stage brings 32 KB into
+// an SM instead of the 48 KB of a 128 x 256 tile, which the SM's 64 bytes a clock from L2
+// could not deliver in the MMAs' 512 clocks.  Each block loads its part (warp 0); the
+// block of rank 0 issues for both (warp 1); each takes its 128 rows of the accumulator
+// out (warps 2..).  Stages are counted on rank 0's barriers, freed on both.
+constexpr int BN2 = 256, STAGES2 = 6, STAGE2_BYTES = 2 * BM * BK * 2;
+constexpr uint32_t IDESC2 = idesc_bf16(256, BN2, 0, 0);
+constexpr int smem2(int mode) { return 1024 + STAGES2 * STAGE2_BYTES + tcg::Cfg<BN2>::stg(mode) + 256; }
+static_assert(smem2(EPI_RESID) <= 232448 && smem2(EPI_GELU) <= 232448, "shared memory of one block");
+enum : unsigned { SITE2_EMPTY = 0x411, SITE2_FULL = 0x412, SITE2_TFULL = 0x413, SITE2_TEMPTY = 0x414, SITE2_DRAIN = 0x415 };
+
+template <int MODE>
+__global__ void __launch_bounds__(tcg::threads<MODE>(), 1)
+k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+             const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmT,
+             const __grid_constant__ CUtensorMap tmU, const Epi ep, const __grid_constant__ Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + STAGES2 * BM * BK * 2;
+  float* stg = reinterpret_cast<float*>(smem + STAGES2 * STAGE2_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES2 * STAGE2_BYTES + tcg::Cfg<BN2>::stg(MODE));   // of rank 0
+  uint64_t* empty = full + STAGES2;      // of each block
+  uint64_t* tfull = empty + STAGES2;     // [2], of each block
+  uint64_t* tempty = tfull + 2;          // [2], of rank 0
+  uint64_t* tdone = tempty + 2;          // of each block
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdone + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int n_tiles = a.N / BN2, tiles = a.m_tiles * n_tiles;
+  const int k_iters = (a.K + BK - 1) / BK;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const Extra ex{a, &tmT, &tmU};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES2; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 2 * 4 * tcg::epi_wg<MODE>()); }
+    mbar_init(tdone, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) { tmem_alloc2(tmem_slot, 512); tmem_relinquish2(); }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap* ta, int ac, int ar, const CUtensorMap* tb, int bc, int br) -> bool {
+        if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, SITE2_EMPTY)) return ok = false;
+        if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * STAGE2_BYTES);   // both blocks' bytes
+        const uint32_t bar = cluster_addr(&full[stage], 0);
+        tma_load_2d_pair(sA + stage * (BM * BK * 2), ta, ac, ar + rank * BM, bar);
+        tma_load_2d_pair(sB + stage * (BM * BK * 2), tb, bc, br + rank * BM, bar);
+        if (++stage == STAGES2) { stage = 0; phase ^= 1u; }
+        return true;
+      };
+      for (int t = first; t < tiles && ok; t += step) {
+        const int m0 = t / n_tiles * 256, n0 = t % n_tiles * BN2;
+        for (int k = 0; k < k_iters; ++k)
+          if (!load(&tmA, k * BK, m0, &tmB, k * BK, n0)) break;
+        ex.wait();
+        if (ok) ex.each(ex.row(t / n_tiles), n0, load);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      const uint64_t da0 = sdesc_sw128(smem_u32(sA), 16, 1024), db0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+      const uint32_t a_lo0 = static_cast<uint32_t>(da0), b_lo0 = static_cast<uint32_t>(db0);
+      const uint32_t d_hi = static_cast<uint32_t>(da0 >> 32);
+      for (int t = first; t < tiles && ok; t += step) {
+        if (!mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, SITE2_TEMPTY)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + acc * BN2;
+        Extra::Row row{};
+        if (t != first) row = ex.row(t / n_tiles);
+        for (int k = 0; k < k_iters; ++k) {
+          if (!mbar_wait_cluster(&full[stage], phase, SITE2_FULL)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_lo = a_lo0 + stage * (BM * BK * 2 >> 4), b_lo = b_lo0 + stage * (BM * BK * 2 >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) umma2_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, IDESC2, (k | kk) != 0);
+          umma2_commit(&empty[stage]);
+          if (++stage == STAGES2) { stage = 0; phase ^= 1u; }
+        }
+        if (t == first) { ex.wait(); row = ex.row(t / n_tiles); }
+        const int extra = ok ? ex.count(row) : 0;
+        for (int k = 0; k < extra; ++k) {
+          if (!mbar_wait_cluster(&full[stage], phase, SITE2_FULL)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_lo = a_lo0 + stage * (BM * BK * 2 >> 4), b_lo = b_lo0 + stage * (BM * BK * 2 >> 4);
+          const int steps = ex.steps(k);
+          for (int kk = 0; kk < steps; ++kk) umma2_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, IDESC2, 1u);
+          umma2_commit(&empty[stage]);
+          if (++stage == STAGES2) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        umma2_commit(&tfull[acc]);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+      umma2_commit(tdone);   // arrives in both blocks once every MMA has read its operands
+    }
+    __syncwarp();
+  } else {
+    constexpr int COLS = BN2 / tcg::epi_wg<MODE>();
+    const int c_begin = ((warp - 2) >> 2) * COLS;
+    int acc = 0;
+    uint32_t acc_phase = 0, chunk = 0;
+    for (int t = first; t < tiles; t += step) {
+      const bool ok = mbar_wait_cluster(&tfull[acc], acc_phase, SITE2_TFULL);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      tcg::epi_tile<BN2, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN2, t / n_tiles * 256 + rank * BM,
+                               t % n_tiles * BN2, a.M, chunk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    if (lane == 0) bulk_wait_group<0>();   // stores and reductions performed before exit
+  }
+  // Every copy has landed (its stage was multiplied) and every MMA has ended before a block leaves.
+  if (warp == 1) {
+    if (lane == 0) mbar_wait_cluster(tdone, 0, SITE2_DRAIN);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc2(tmem, 512);
+}
+
 // ------------------------------------------------------------------ T = scale A D^T
-// One cluster of `split` blocks per slab, each with a share of K: 128 rows x rank, K in
+// One cluster of `split` blocks per 128 rows of a slab, each with a share of K: 128 rows x rank, K in
 // 64-wide TMA stages, tcgen05 MMAs of 128 x RN x 16 (RN = rank rounded up to 16; the
 // rows of D behind rank belong to the next adapter and their columns are not stored).
 // Warp 0 loads, warp 1 issues, warps 2-5 take the accumulator out.  The blocks'
@@ -153,9 +298,6 @@ static_assert(BM * (MAX_RANK + 4) * 4 <= STAGES * stage_bytes(MAX_RANK) && BM * 
 
 enum : unsigned { SITE_EMPTY = 0x401, SITE_FULL = 0x402, SITE_DONE = 0x403, SITE_DRAIN = 0x404 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // 16 bytes at shared address `addr` of block `rank` of the cluster
 __device__ __forceinline__ float4 cluster_ld4(uint32_t addr, uint32_t rank) {
   uint32_t peer;
@@ -174,18 +316,26 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   __shared__ uint64_t full[STAGES], empty[STAGES], done;
   __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slab = blockIdx.x / split, part = blockIdx.x % split;
+  const int halves = a.tile / BM, part = blockIdx.x % split, half = blockIdx.x / split % halves, slab = blockIdx.x / split / halves;
 
   if (threadIdx.x == 0) { tma_prefetch_desc(&tmA); tma_prefetch_desc(&tmD); }
   // the pair (m, s) of this slab: the last s whose request starts before the end of tile slab - s
-  const int s = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] < (slab - s + 1) * BM; });
-  const int m = slab - s, m0 = m * BM;
-  const bool lists = slab < a.m_tiles && part == 0 && warp == 5;   // this warp also writes tile `slab`'s list
+  const int s = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] < (slab - s + 1) * a.tile; });
+  const int m = slab - s, m0 = m * a.tile + half * BM;
+  const bool lists = slab < a.m_tiles && part == 0 && half == 0 && warp == 5;   // this warp also writes tile `slab`'s list
   int2 rows_s = make_int2(0, 0);
   int ad = -1;
   if (s >= 0) { rows_s = seg_rows(a, s); ad = a.ids[s]; }
-  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, rows_s, ad, m0)) {   // no such pair: the whole cluster leaves
+  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, rows_s, ad, m * a.tile)) {   // no such pair: the whole cluster leaves
     if (lists) write_list(a, slab, lane);
+    return;
+  }
+  bf16* dst = a.slabs + (static_cast<int64_t>(slab) * a.parts * a.tile + half * BM) * a.rank;
+  const int64_t rem = static_cast<int64_t>(a.tile) * a.rank;   // from the high part to the remainder
+  if (max(rows_s.x, m0) >= min(rows_s.y, m0 + BM)) {           // the request lies in the tile's other half: zeros
+    if (lists) write_list(a, slab, lane);
+    for (int i = part * THREADS + threadIdx.x; i < BM * a.rank / 8; i += split * THREADS)
+      for (int p = 0; p < a.parts; ++p) reinterpret_cast<uint4*>(dst + p * rem)[i] = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
   const int k_iters = (a.K + BK - 1) / BK;
@@ -291,9 +441,9 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       const float2 f = unpack_bf16x2(w[j]);
       x[j] = pack_bf16x2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
     }
-    bf16* out = a.slabs + (static_cast<int64_t>(slab) * a.parts * BM + r) * a.rank + c;
+    bf16* out = dst + r * a.rank + c;
     *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (a.parts == 2) *reinterpret_cast<uint4*>(out + static_cast<int64_t>(BM) * a.rank) = make_uint4(x[0], x[1], x[2], x[3]);
+    if (a.parts == 2) *reinterpret_cast<uint4*>(out + rem) = make_uint4(x[0], x[1], x[2], x[3]);
   }
   cluster_sync();   // no block leaves while others read its part
 }
@@ -301,36 +451,52 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 }  // namespace lora
 
 // ------------------------------------------------------------------ host side
-static size_t lora_slab_bytes(int64_t slabs, int rank) { return static_cast<size_t>(slabs) * 2 * lora::BM * rank * 2; }
+static size_t lora_slab_bytes(int64_t slabs, int tile, int rank) { return static_cast<size_t>(slabs) * 2 * tile * rank * 2; }
 
 size_t gemm_lora_bytes(int M, int n_seg, int rank) {
-  const int64_t mt = (static_cast<int64_t>(M) + lora::BM - 1) / lora::BM;
-  return lora_slab_bytes(mt + n_seg, rank) + static_cast<size_t>(mt) * sizeof(int4) + static_cast<size_t>(mt + n_seg) * sizeof(int2);
+  size_t most = 0;
+  for (int tile : {128, 256}) {
+    const int64_t mt = (static_cast<int64_t>(M) + tile - 1) / tile;
+    const size_t n = lora_slab_bytes(mt + n_seg, tile, rank) + static_cast<size_t>(mt) * sizeof(int4) + static_cast<size_t>(mt + n_seg) * sizeof(int2);
+    if (n > most) most = n;
+  }
+  return most;
 }
+
+constexpr int LORA_PAIR = 512;   // the "tile width" of k_gemm_lora2 in the dispatch
 
 template <int BN, int MODE>
 static wd_status launch_lora(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tt, const CUtensorMap& tu,
                              const Epi& ep, const lora::Args& a, cudaStream_t st) {
-  using C = tcg::Cfg<BN>;
-  WD_TRY((allow_smem<lora::k_gemm_lora<BN, MODE>>(C::smem(MODE))));
-  const int tiles = a.m_tiles * (a.N / BN);
-  const int grid = tiles < sm_count() ? tiles : sm_count();
+  constexpr bool PAIR = BN == LORA_PAIR;
+  constexpr int W = PAIR ? 256 : BN;
+  constexpr int SMEM = PAIR ? lora::smem2(MODE) : tcg::Cfg<W>::smem(MODE);
+  const int tiles = a.m_tiles * (a.N / W), at_once = PAIR ? sm_count() / 2 : sm_count();
   CUtensorMap tx = ta;
   if (MODE == EPI_RESID) WD_TRY(make_tmap_f32(&tx, ep.out, a.M, a.N, ep.ldo, 32, 32));
-  if (tcg::staged2<MODE>() && (BN / tcg::epi_wg<MODE>()) % 64 == 0)
+  if (tcg::staged2<MODE>() && (W / tcg::epi_wg<MODE>()) % 64 == 0)
     WD_TRY(make_tmap_2b(&tx, ep.out, a.M, a.N, ep.ldo, MODE == EPI_STORE_F16));
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // may start before k_lora_down has ended: Extra::wait
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3((tiles < at_once ? tiles : at_once) * (PAIR ? 2 : 1));
   cfg.blockDim = dim3(tcg::threads<MODE>());
-  cfg.dynamicSmemBytes = C::smem(MODE);
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
-  cudaLaunchAttribute early{};   // may start before k_lora_down has ended; waits for it in Extra::wait
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
   Trace tr(KC_GEMM, st);
-  cudaLaunchKernelEx(&cfg, lora::k_gemm_lora<BN, MODE>, ta, tb, tx, tt, tu, ep, a);
+  if constexpr (PAIR) {
+    WD_TRY((allow_smem<lora::k_gemm_lora2<MODE>>(SMEM)));
+    cudaLaunchKernelEx(&cfg, lora::k_gemm_lora2<MODE>, ta, tb, tx, tt, tu, ep, a);
+  } else {
+    WD_TRY((allow_smem<lora::k_gemm_lora<W, MODE>>(SMEM)));
+    cudaLaunchKernelEx(&cfg, lora::k_gemm_lora<W, MODE>, ta, tb, tx, tt, tu, ep, a);
+  }
   return launch_status("gemm_lora");
 }
 
@@ -348,15 +514,19 @@ static wd_status dispatch_lora(int mode, const CUtensorMap& ta, const CUtensorMa
   return WD_ERR_ARG;
 }
 
-// Tile width: the time of a round of tiles goes with the bytes of a K stage, 128 + BN
-// rows, so the width with the least rounds * (128 + BN) is taken.
-static int lora_tile(int m_tiles, int N) {
+// Tile: the time of a round of tiles goes with the bytes of a K stage that an SM takes in, 128 + BN
+// rows of A and B for a tile of 128 x BN and 128 + 128 for an SM pair's 256 x 256 (BN = 512
+// here), so the tile with the least rounds * rows is taken; at equal cost the narrower one, whose
+// row tiles are shorter.
+static int lora_tile(int M, int N) {
   int best = 64;
   int64_t least = INT64_MAX;
-  for (int bn = 256; bn >= 64; bn /= 2) {
-    if (N % bn) continue;
-    const int64_t tiles = static_cast<int64_t>(m_tiles) * (N / bn), rounds = (tiles + sm_count() - 1) / sm_count();
-    if (rounds * (128 + bn) < least) { least = rounds * (128 + bn); best = bn; }
+  for (int bn : {64, 128, 256, LORA_PAIR}) {
+    const bool pair = bn == LORA_PAIR;
+    if (N % (pair ? 256 : bn)) continue;
+    const int64_t tiles = pair ? (M + 255ll) / 256 * (N / 256) : (M + 127ll) / 128 * (N / bn);
+    const int64_t at_once = pair ? sm_count() / 2 : sm_count(), cost = (tiles + at_once - 1) / at_once * (pair ? 256 : 128 + bn);
+    if (cost < least) { least = cost; best = bn; }
   }
   return best;
 }
@@ -368,10 +538,13 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   a.n_seg = l.n_seg; a.n_adapters = l.n_adapters; a.rank = l.rank;
   a.parts = (mode == EPI_F32 || mode == EPI_RESID) ? 2 : 1;
   a.M = M; a.N = N; a.K = K;
-  a.m_tiles = (M + lora::BM - 1) / lora::BM;
+  const int BN = lora_tile(M, N);
+  const bool pair = BN == LORA_PAIR;
+  a.tile = pair ? 256 : 128;
+  a.m_tiles = static_cast<int>((static_cast<int64_t>(M) + a.tile - 1) / a.tile);
   const int64_t slabs = static_cast<int64_t>(a.m_tiles) + l.n_seg;
   a.slabs = static_cast<bf16*>(ws);
-  a.tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + lora_slab_bytes(slabs, l.rank));   // a multiple of 4096 bytes on
+  a.tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + lora_slab_bytes(slabs, a.tile, l.rank));   // a multiple of 4096 bytes on
   a.list = reinterpret_cast<int2*>(a.tiles + a.m_tiles);
   const int rn = (l.rank + 15) / 16 * 16;
   CUtensorMap ta, tb, td, tt, tu;
@@ -384,9 +557,10 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
     // enough blocks to fill the SMs twice over, with 4 stages of K each at least
     int split = 1;
     const int k_iters = (K + lora::BK - 1) / lora::BK;
-    while (split < lora::MAX_SPLIT && slabs * split < 2 * sm_count() && k_iters >= 8 * split) split *= 2;
+    const int64_t blocks = slabs * (a.tile / lora::BM);
+    while (split < lora::MAX_SPLIT && blocks * split < 2 * sm_count() && k_iters >= 8 * split) split *= 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(slabs * split));
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks * split));
     cfg.blockDim = dim3(lora::THREADS);
     cfg.dynamicSmemBytes = lora::smem_bytes(rn);
     cfg.stream = st;
@@ -400,11 +574,12 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
     cudaLaunchKernelEx(&cfg, lora::k_lora_down, ta, td, a, rn, cols, idesc_bf16(lora::BM, rn, 0, 0), split);
   }
   WD_TRY(launch_status("lora_down"));
-  const int BN = lora_tile(a.m_tiles, N);
-  WD_TRY(make_tmap_bf16(&tb, W, N, K, K, lora::BK, BN));
-  WD_TRY(make_tmap_bf16(&tt, a.slabs, slabs * a.parts * lora::BM, l.rank, l.rank, lora::BK, lora::BM));
-  WD_TRY(make_tmap_bf16(&tu, l.up, static_cast<int64_t>(l.n_adapters) * N, l.rank, l.rank, lora::BK, BN));
+  const int rows_b = pair ? lora::BM : BN;   // of B a load brings: an SM of a pair loads half
+  WD_TRY(make_tmap_bf16(&tb, W, N, K, K, lora::BK, rows_b));
+  WD_TRY(make_tmap_bf16(&tt, a.slabs, slabs * a.parts * a.tile, l.rank, l.rank, lora::BK, lora::BM));
+  WD_TRY(make_tmap_bf16(&tu, l.up, static_cast<int64_t>(l.n_adapters) * N, l.rank, l.rank, lora::BK, rows_b));
   switch (BN) {
+    case LORA_PAIR: return dispatch_lora<LORA_PAIR>(mode, ta, tb, tt, tu, ep, a, st);
     case 256: return dispatch_lora<256>(mode, ta, tb, tt, tu, ep, a, st);
     case 128: return dispatch_lora<128>(mode, ta, tb, tt, tu, ep, a, st);
     default: return dispatch_lora<64>(mode, ta, tb, tt, tu, ep, a, st);

@@ -141,6 +141,103 @@ __device__ __forceinline__ void epilogue32(const Epi& ep, int64_t m, int n, cons
   }
 }
 
+// ------------------------------------------------------------------ epilogue of one tile
+// One epilogue warp: its 32 rows (TMEM lane quarter warp & 3) of the 128-row tile at
+// (m0, n0) whose accumulator begins at TMEM column acc, columns c_begin ... of its
+// warpgroup's share; chunk counts the staging tiles used so far.
+template <int BN, int MODE>
+__device__ __forceinline__ void epi_tile(const Epi& ep, const CUtensorMap& tmX, float* stg, int warp, int lane, int c_begin,
+                                         uint32_t acc, int m0, int n0, int M, uint32_t& chunk) {
+  constexpr int COLS = BN / epi_wg<MODE>();
+  const int q = warp & 3;
+  const int64_t m = m0 + q * 32 + lane;
+  const uint32_t tbase = acc + (static_cast<uint32_t>(q * 32) << 16);
+  if constexpr (MODE == EPI_RESID) {
+    // X[m, n] += g[n] * v through the TMA: this warp's 32 rows x 32 columns
+    // go to a 128-byte-swizzled staging tile (row `lane`, 16-byte chunk j
+    // at chunk j ^ (lane & 7)), then one lane reduces the tile into X in
+    // L2, so no residual load waits in the SM.
+    const bool gated = ep.gate_a || ep.gate_b;
+    // FP8 row scale of this thread's row, read once per tile (inside the column loop the
+    // compiler cannot keep it across the staging-tile stores)
+    const float rs = (ep.sa && m < M) ? ep.sa[m] : 0.f;
+#pragma unroll 1
+    for (int c = c_begin; c < c_begin + COLS; c += 32) {
+      uint32_t r[32];
+      tmem_ld32(tbase + c, r);
+      float* tile = stg + ((warp - 2) * 2 + (chunk & 1)) * (32 * 32);
+      if (lane == 0) bulk_wait_group_read<1>();   // the reduce that last read this tile is done with it
+      __syncwarp();
+      tmem_wait_ld();
+      float4* row = reinterpret_cast<float4*>(tile + lane * 32);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int n = n0 + c + 4 * j;
+        float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (gated) {
+          const float4 ga = ep.gate_a ? __ldg(reinterpret_cast<const float4*>(ep.gate_a + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 gb = ep.gate_b ? __ldg(reinterpret_cast<const float4*>(ep.gate_b + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          g = make_float4(ga.x + gb.x, ga.y + gb.y, ga.z + gb.z, ga.w + gb.w);
+        }
+        const float4 bb = ep.bias ? __ldg(reinterpret_cast<const float4*>(ep.bias + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 a = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                               __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+        if (ep.sa) {   // FP8 operands: acc * (sa[m] * sb[n])
+          const float4 sb = __ldg(reinterpret_cast<const float4*>(ep.sb + n));
+          a.x *= rs * sb.x; a.y *= rs * sb.y; a.z *= rs * sb.z; a.w *= rs * sb.w;
+        }
+        row[j ^ (lane & 7)] = make_float4(g.x * (a.x + bb.x), g.y * (a.y + bb.y), g.z * (a.z + bb.z), g.w * (a.w + bb.w));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && m0 + q * 32 < M) {   // rows past M inside the box are skipped by the TMA
+        tma_reduce_add_2d(tile, &tmX, n0 + c, m0 + q * 32);
+        bulk_commit_group();
+      }
+      ++chunk;
+    }
+  } else if constexpr (staged2<MODE>() && COLS % 64 == 0) {
+    // 64 columns at a time: values packed into this warp's staging tile
+    // (row `lane`, 16-byte chunk j at chunk j ^ (lane & 7)), then one lane
+    // stores the 32 x 64 box; rows past M inside the box are clipped by the TMA.
+    constexpr int NB = stg_bufs<MODE>();
+    const float sm = (ep.sa && m < M) ? ep.sa[m] : 0.f;
+#pragma unroll 1
+    for (int c = c_begin; c < c_begin + COLS; c += 64) {
+      uint32_t r0[32], r1[32];
+      tmem_ld32(tbase + c, r0);
+      tmem_ld32(tbase + c + 32, r1);
+      uint8_t* tile = reinterpret_cast<uint8_t*>(stg) + ((warp - 2) * NB + (chunk % NB)) * STG2_TILE;
+      if (lane == 0) bulk_wait_group_read<NB - 1>();   // the store that last read this tile is done with it
+      __syncwarp();
+      tmem_wait_ld();
+      uint4* row = reinterpret_cast<uint4*>(tile + lane * 128);
+      float v[32];
+      epi_values32<MODE>(ep, sm, n0 + c, r0, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) row[j ^ (lane & 7)] = pack8<MODE>(v + 8 * j);
+      epi_values32<MODE>(ep, sm, n0 + c + 32, r1, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) row[(4 + j) ^ (lane & 7)] = pack8<MODE>(v + 8 * j);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && m0 + q * 32 < M) {
+        tma_store_2d(tile, &tmX, n0 + c, m0 + q * 32);
+        bulk_commit_group();
+      }
+      ++chunk;
+    }
+  } else {
+#pragma unroll 1
+    for (int c = c_begin; c < c_begin + COLS; c += 32) {
+      uint32_t r[32];
+      tmem_ld32(tbase + c, r);
+      tmem_wait_ld();
+      if (m < M) epilogue32<MODE>(ep, m, n0 + c, r);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 // Further K-blocks of a row tile, accumulated after the K loop of A and B: none
 // for the plain GEMM; the low-rank products of k_gemm_lora.cu implement these.
@@ -280,102 +377,16 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     __syncwarp();
   } else {
     // ---------------------------------------------------------- epilogue warps
-    const int q = warp & 3;   // TMEM lane quarter this warp may access
     constexpr int COLS = BN / epi_wg<MODE>();
     const int c_begin = ((warp - 2) >> 2) * COLS;
     int acc = 0;
     uint32_t acc_phase = 0;
-    [[maybe_unused]] uint32_t chunk = 0;   // residual staging tiles used so far (alternating)
+    uint32_t chunk = 0;   // staging tiles used so far (alternating)
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const int m0 = (t / n_tiles) * BM, n0 = (t % n_tiles) * BN;
       if (!mbar_wait_warp(&tfull[acc], acc_phase, SITE_TFULL)) break;
       tc_fence_after();
-      const int64_t m = m0 + q * 32 + lane;
-      const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
-      if constexpr (MODE == EPI_RESID) {
-        // X[m, n] += g[n] * v through the TMA: this warp's 32 rows x 32 columns
-        // go to a 128-byte-swizzled staging tile (row `lane`, 16-byte chunk j
-        // at chunk j ^ (lane & 7)), then one lane reduces the tile into X in
-        // L2, so no residual load waits in the SM.
-        const bool gated = ep.gate_a || ep.gate_b;
-        // FP8 row scale of this thread's row, read once per tile (inside the column loop the
-        // compiler cannot keep it across the staging-tile stores)
-        const float rs = (ep.sa && m < M) ? ep.sa[m] : 0.f;
-#pragma unroll 1
-        for (int c = c_begin; c < c_begin + COLS; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(tbase + c, r);
-          float* tile = stg + ((warp - 2) * 2 + (chunk & 1)) * (32 * 32);
-          if (lane == 0) bulk_wait_group_read<1>();   // the reduce that last read this tile is done with it
-          __syncwarp();
-          tmem_wait_ld();
-          float4* row = reinterpret_cast<float4*>(tile + lane * 32);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int n = n0 + c + 4 * j;
-            float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (gated) {
-              const float4 ga = ep.gate_a ? __ldg(reinterpret_cast<const float4*>(ep.gate_a + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
-              const float4 gb = ep.gate_b ? __ldg(reinterpret_cast<const float4*>(ep.gate_b + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
-              g = make_float4(ga.x + gb.x, ga.y + gb.y, ga.z + gb.z, ga.w + gb.w);
-            }
-            const float4 bb = ep.bias ? __ldg(reinterpret_cast<const float4*>(ep.bias + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            float4 a = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                   __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-            if (ep.sa) {   // FP8 operands: acc * (sa[m] * sb[n])
-              const float4 sb = __ldg(reinterpret_cast<const float4*>(ep.sb + n));
-              a.x *= rs * sb.x; a.y *= rs * sb.y; a.z *= rs * sb.z; a.w *= rs * sb.w;
-            }
-            row[j ^ (lane & 7)] = make_float4(g.x * (a.x + bb.x), g.y * (a.y + bb.y), g.z * (a.z + bb.z), g.w * (a.w + bb.w));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && m0 + q * 32 < M) {   // rows past M inside the box are skipped by the TMA
-            tma_reduce_add_2d(tile, &tmX, n0 + c, m0 + q * 32);
-            bulk_commit_group();
-          }
-          ++chunk;
-        }
-      } else if constexpr (staged2<MODE>() && COLS % 64 == 0) {
-        // 64 columns at a time: values packed into this warp's staging tile
-        // (row `lane`, 16-byte chunk j at chunk j ^ (lane & 7)), then one lane
-        // stores the 32 x 64 box; rows past M inside the box are clipped by the TMA.
-        constexpr int NB = stg_bufs<MODE>();
-        const float sm = (ep.sa && m < M) ? ep.sa[m] : 0.f;
-#pragma unroll 1
-        for (int c = c_begin; c < c_begin + COLS; c += 64) {
-          uint32_t r0[32], r1[32];
-          tmem_ld32(tbase + c, r0);
-          tmem_ld32(tbase + c + 32, r1);
-          uint8_t* tile = reinterpret_cast<uint8_t*>(stg) + ((warp - 2) * NB + (chunk % NB)) * STG2_TILE;
-          if (lane == 0) bulk_wait_group_read<NB - 1>();   // the store that last read this tile is done with it
-          __syncwarp();
-          tmem_wait_ld();
-          uint4* row = reinterpret_cast<uint4*>(tile + lane * 128);
-          float v[32];
-          epi_values32<MODE>(ep, sm, n0 + c, r0, v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) row[j ^ (lane & 7)] = pack8<MODE>(v + 8 * j);
-          epi_values32<MODE>(ep, sm, n0 + c + 32, r1, v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) row[(4 + j) ^ (lane & 7)] = pack8<MODE>(v + 8 * j);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && m0 + q * 32 < M) {
-            tma_store_2d(tile, &tmX, n0 + c, m0 + q * 32);
-            bulk_commit_group();
-          }
-          ++chunk;
-        }
-      } else {
-#pragma unroll 1
-        for (int c = c_begin; c < c_begin + COLS; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(tbase + c, r);
-          tmem_wait_ld();
-          if (m < M) epilogue32<MODE>(ep, m, n0 + c, r);
-        }
-      }
+      epi_tile<BN, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN, m0, n0, M, chunk);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[acc]);

@@ -732,3 +732,12 @@ def test_offsets_past_32_bits(wd):
     wd.wd_check()
     v, err = lora64(A[-200:], W, torch.zeros(N, device="cuda"), [0, 50, 180], ids, down, up, None, 1)
     assert_within(out[-200:], v, err * (1 + 2.0 ** -8) + 2.0 ** -8 * v.abs())
+
+
+@pytest.mark.parametrize("epi", [0, 1, 2, 3, 5])
+@pytest.mark.parametrize("M,N,K,rank", [(20000, 256, 136, 16), (19001, 512, 1536, 40), (30000, 256, 64, 136)])
+def test_gemm_lora_sm_pairs(wd, epi, M, N, K, rank):
+    """Shapes that run on SM pairs (256 x 256 tiles): requests that end inside either half
+    of a tile, lie in one half only, or cover several tiles; rows of none at both ends."""
+    lens = [1, 127, 128, 200, 3, 0, 56, 600, 5000, 130, 126, 1, 9000]
+    run_lora(wd, lens, [0, 1, 2, -1, 1, 0, 2, 0, 1, 2, 0, 1, 0], M, N, K, rank, 3, epi, start=70)
