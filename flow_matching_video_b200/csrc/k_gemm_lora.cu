@@ -18,9 +18,10 @@
 // monotone chain and m + s numbers the slabs without a table.
 //
 // T enters the second product in bf16, rounded once when the output has 2 bytes
-// (its own rounding is as large).  For fp32 outputs T is split in two bf16
-// parts, high and remainder, and both are multiplied: 2^-17 of the adapter's share
-// is lost instead of 2^-9.
+// (its own rounding is as large).  For fp32 outputs T is split in three bf16 parts,
+// each the remainder of those before, and all are multiplied: 2^-26 of the adapter's
+// share is lost instead of 2^-9; and the accumulator is summed in registers every 8
+// stages of K (sum_every in k_gemm_tc.cu).
 #include "wd_internal.cuh"
 
 namespace wd {
@@ -96,6 +97,8 @@ __device__ __forceinline__ void write_list(const Args& a, int m, int lane) {
 // The extra K-blocks of gemm_body: request after request, part after part.
 struct Extra {
   static constexpr bool ON = true;
+  template <int MODE> __host__ __device__ static constexpr int sum_every() { return MODE == EPI_F32 || MODE == EPI_RESID ? 8 : 0; }
+  template <int MODE> __host__ __device__ static constexpr int wg() { return sum_every<MODE>() ? 2 : tcg::epi_wg<MODE>(); }
   const Args& a;
   const CUtensorMap* tmT;   // slabs [rows, rank], box 64 x 128
   const CUtensorMap* tmU;   // U [n_adapters * N, rank], box 64 x BN
@@ -128,8 +131,14 @@ struct Extra {
   }
 };
 
+template <int MODE> __host__ __device__ constexpr int threads() { return 64 + 128 * Extra::wg<MODE>(); }
+// staging: one 32 x 32 fp32 tile a warp, or as k_gemm_tc's
+template <int BN, int MODE> __host__ __device__ constexpr int staging() {
+  return Extra::sum_every<MODE>() ? 8 * 4096 : tcg::Cfg<BN>::stg(MODE);
+}
+
 template <int BN, int MODE>
-__global__ void __launch_bounds__(tcg::threads<MODE>(), 1)
+__global__ void __launch_bounds__(threads<MODE>(), 1)
 k_gemm_lora(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmT,
             const __grid_constant__ CUtensorMap tmU, const Epi ep, const __grid_constant__ Args a) {
@@ -145,12 +154,12 @@ k_gemm_lora(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 // out (warps 2..).  Stages are counted on rank 0's barriers, freed on both.
 constexpr int BN2 = 256, STAGES2 = 6, STAGE2_BYTES = 2 * BM * BK * 2;
 constexpr uint32_t IDESC2 = idesc_bf16(256, BN2, 0, 0);
-constexpr int smem2(int mode) { return 1024 + STAGES2 * STAGE2_BYTES + tcg::Cfg<BN2>::stg(mode) + 256; }
-static_assert(smem2(EPI_RESID) <= 232448 && smem2(EPI_GELU) <= 232448, "shared memory of one block");
+template <int MODE> constexpr int smem2() { return 1024 + STAGES2 * STAGE2_BYTES + staging<BN2, MODE>() + 256; }
+static_assert(smem2<EPI_F32>() <= 232448 && smem2<EPI_GELU>() <= 232448, "shared memory of one block");
 enum : unsigned { SITE2_EMPTY = 0x411, SITE2_FULL = 0x412, SITE2_TFULL = 0x413, SITE2_TEMPTY = 0x414, SITE2_DRAIN = 0x415 };
 
 template <int MODE>
-__global__ void __launch_bounds__(tcg::threads<MODE>(), 1)
+__global__ void __launch_bounds__(threads<MODE>(), 1)
 k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmT,
              const __grid_constant__ CUtensorMap tmU, const Epi ep, const __grid_constant__ Args a) {
@@ -159,7 +168,7 @@ k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES2 * BM * BK * 2;
   float* stg = reinterpret_cast<float*>(smem + STAGES2 * STAGE2_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES2 * STAGE2_BYTES + tcg::Cfg<BN2>::stg(MODE));   // of rank 0
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES2 * STAGE2_BYTES + staging<BN2, MODE>());   // of rank 0
   uint64_t* empty = full + STAGES2;      // of each block
   uint64_t* tfull = empty + STAGES2;     // [2], of each block
   uint64_t* tempty = tfull + 2;          // [2], of rank 0
@@ -170,11 +179,12 @@ k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
   const int n_tiles = a.N / BN2, tiles = a.m_tiles * n_tiles;
   const int k_iters = (a.K + BK - 1) / BK;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  constexpr int SUM = Extra::sum_every<MODE>();
   const Extra ex{a, &tmT, &tmU};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES2; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 2 * 4 * tcg::epi_wg<MODE>()); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 2 * 4 * Extra::wg<MODE>()); }
     mbar_init(tdone, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
@@ -221,15 +231,24 @@ k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
       for (int t = first; t < tiles && ok; t += step) {
         if (!mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, SITE2_TEMPTY)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t d = tmem + acc * BN2;
+        uint32_t d = tmem + acc * BN2;
         Extra::Row row{};
         if (t != first) row = ex.row(t / n_tiles);
         for (int k = 0; k < k_iters; ++k) {
+          if constexpr (SUM > 0) {
+            if (k && k % SUM == 0) {   // hand this part over and go on in the other accumulator
+              umma2_commit(&tfull[acc]);
+              if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+              if (!mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, SITE2_TEMPTY)) { ok = false; break; }
+              tc_fence_after();
+              d = tmem + acc * BN2;
+            }
+          }
           if (!mbar_wait_cluster(&full[stage], phase, SITE2_FULL)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_lo = a_lo0 + stage * (BM * BK * 2 >> 4), b_lo = b_lo0 + stage * (BM * BK * 2 >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) umma2_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, IDESC2, (k | kk) != 0);
+          for (int kk = 0; kk < BK / 16; ++kk) umma2_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, IDESC2, ((SUM ? k % (SUM ? SUM : 1) : k) | kk) != 0);
           umma2_commit(&empty[stage]);
           if (++stage == STAGES2) { stage = 0; phase ^= 1u; }
         }
@@ -252,20 +271,40 @@ k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     }
     __syncwarp();
   } else {
-    constexpr int COLS = BN2 / tcg::epi_wg<MODE>();
-    const int c_begin = ((warp - 2) >> 2) * COLS;
+    constexpr int COLS = BN2 / Extra::wg<MODE>();
+    const int c_begin = ((warp - 2) >> 2) * COLS, q = warp & 3;
     int acc = 0;
-    uint32_t acc_phase = 0, chunk = 0;
-    for (int t = first; t < tiles; t += step) {
+    uint32_t acc_phase = 0;
+    [[maybe_unused]] uint32_t chunk = 0;
+    auto wait = [&]() -> bool {
       const bool ok = mbar_wait_cluster(&tfull[acc], acc_phase, SITE2_TFULL);
-      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      tcg::epi_tile<BN2, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN2, t / n_tiles * 256 + rank * BM,
-                               t % n_tiles * BN2, a.M, chunk);
+      return __all_sync(0xffffffffu, ok);
+    };
+    auto release = [&]() {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    };
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      const int m0 = t / n_tiles * 256 + rank * BM, n0 = t % n_tiles * BN2;
+      if constexpr (SUM > 0) {
+        float v[COLS];
+        for (int k = 0; k < k_iters && ok; k += SUM) {
+          ok = wait();
+          if (!ok) break;
+          tcg::add_columns(tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN2 + c_begin, v, k == 0);
+          release();
+        }
+        if (ok) tcg::epi_sums<MODE>(ep, tmX, stg + (warp - 2) * 1024, lane, v, m0 + q * 32, n0 + c_begin, a.M);
+      } else {
+        ok = wait();
+        if (!ok) break;
+        tcg::epi_tile<BN2, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN2, m0, n0, a.M, chunk);
+        release();
+      }
     }
     if (lane == 0) bulk_wait_group<0>();   // stores and reductions performed before exit
   }
@@ -331,11 +370,11 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     return;
   }
   bf16* dst = a.slabs + (static_cast<int64_t>(slab) * a.parts * a.tile + half * BM) * a.rank;
-  const int64_t rem = static_cast<int64_t>(a.tile) * a.rank;   // from the high part to the remainder
+  const int64_t next = static_cast<int64_t>(a.tile) * a.rank;   // from one part to the next
   if (max(rows_s.x, m0) >= min(rows_s.y, m0 + BM)) {           // the request lies in the tile's other half: zeros
     if (lists) write_list(a, slab, lane);
     for (int i = part * THREADS + threadIdx.x; i < BM * a.rank / 8; i += split * THREADS)
-      for (int p = 0; p < a.parts; ++p) reinterpret_cast<uint4*>(dst + p * rem)[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int p = 0; p < a.parts; ++p) reinterpret_cast<uint4*>(dst + p * next)[i] = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
   const int k_iters = (a.K + BK - 1) / BK;
@@ -434,16 +473,17 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= sc;
     }
-    uint32_t w[4], x[4];
+    for (int p = 0; p < a.parts; ++p) {
+      uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-      const float2 f = unpack_bf16x2(w[j]);
-      x[j] = pack_bf16x2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+      for (int j = 0; j < 4; ++j) {   // rounded, and the exact remainder kept for the next part
+        w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        const float2 f = unpack_bf16x2(w[j]);
+        v[2 * j] -= f.x;
+        v[2 * j + 1] -= f.y;
+      }
+      *reinterpret_cast<uint4*>(dst + p * next + r * a.rank + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    bf16* out = dst + r * a.rank + c;
-    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (a.parts == 2) *reinterpret_cast<uint4*>(out + rem) = make_uint4(x[0], x[1], x[2], x[3]);
   }
   cluster_sync();   // no block leaves while others read its part
 }
@@ -451,7 +491,7 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 }  // namespace lora
 
 // ------------------------------------------------------------------ host side
-static size_t lora_slab_bytes(int64_t slabs, int tile, int rank) { return static_cast<size_t>(slabs) * 2 * tile * rank * 2; }
+static size_t lora_slab_bytes(int64_t slabs, int tile, int rank) { return static_cast<size_t>(slabs) * 3 * tile * rank * 2; }
 
 size_t gemm_lora_bytes(int M, int n_seg, int rank) {
   size_t most = 0;
@@ -470,10 +510,10 @@ static wd_status launch_lora(const CUtensorMap& ta, const CUtensorMap& tb, const
                              const Epi& ep, const lora::Args& a, cudaStream_t st) {
   constexpr bool PAIR = BN == LORA_PAIR;
   constexpr int W = PAIR ? 256 : BN;
-  constexpr int SMEM = PAIR ? lora::smem2(MODE) : tcg::Cfg<W>::smem(MODE);
+  constexpr int SMEM = PAIR ? lora::smem2<MODE>() : tcg::Cfg<W>::smem(MODE) - tcg::Cfg<W>::stg(MODE) + lora::staging<W, MODE>();
   const int tiles = a.m_tiles * (a.N / W), at_once = PAIR ? sm_count() / 2 : sm_count();
   CUtensorMap tx = ta;
-  if (MODE == EPI_RESID) WD_TRY(make_tmap_f32(&tx, ep.out, a.M, a.N, ep.ldo, 32, 32));
+  if (lora::Extra::sum_every<MODE>()) WD_TRY(make_tmap_f32(&tx, ep.out, a.M, a.N, ep.ldo, 32, 32));
   if (tcg::staged2<MODE>() && (W / tcg::epi_wg<MODE>()) % 64 == 0)
     WD_TRY(make_tmap_2b(&tx, ep.out, a.M, a.N, ep.ldo, MODE == EPI_STORE_F16));
   cudaLaunchAttribute attr[2]{};
@@ -484,7 +524,7 @@ static wd_status launch_lora(const CUtensorMap& ta, const CUtensorMap& tb, const
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((tiles < at_once ? tiles : at_once) * (PAIR ? 2 : 1));
-  cfg.blockDim = dim3(tcg::threads<MODE>());
+  cfg.blockDim = dim3(lora::threads<MODE>());
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -536,7 +576,7 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   lora::Args a{};
   a.seg = l.seg; a.ids = l.adapter; a.scale = l.scale;
   a.n_seg = l.n_seg; a.n_adapters = l.n_adapters; a.rank = l.rank;
-  a.parts = (mode == EPI_F32 || mode == EPI_RESID) ? 2 : 1;
+  a.parts = (mode == EPI_F32 || mode == EPI_RESID) ? 3 : 1;
   a.M = M; a.N = N; a.K = K;
   const int BN = lora_tile(M, N);
   const bool pair = BN == LORA_PAIR;

@@ -244,18 +244,74 @@ __device__ __forceinline__ void epi_tile(const Epi& ep, const CUtensorMap& tmX, 
 struct NoExtra {
   static constexpr bool ON = false;
   using Row = int;
+  template <int MODE> __host__ __device__ static constexpr int wg() { return epi_wg<MODE>(); }   // epilogue warpgroups
+  template <int MODE> __host__ __device__ static constexpr int sum_every() { return 0; }
 };
+
+// sum_every() = S > 0: the accumulator is taken out and started anew every S stages of K,
+// and summed in the epilogue warps' registers (rounded to nearest).  The tensor core's own
+// fp32 accumulation truncates: 64 products lose nothing to speak of, 1536 lose 1.3e-6 and
+// 8960 lose 8.6e-6 of the result, always towards zero.
+template <int COLS>
+__device__ __forceinline__ void add_columns(uint32_t tbase, float (&v)[COLS], bool first) {
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) {
+    uint32_t r[32];
+    tmem_ld32(tbase + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[c + j] = first ? __uint_as_float(r[j]) : v[c + j] + __uint_as_float(r[j]);
+  }
+}
+
+// The fp32 epilogues from registers: one warp's 32 rows x COLS columns from column n on, each
+// 32 x 32 piece through the warp's staging tile (laid out as in epi_tile) and out by a
+// TMA store (EPI_F32) or reduce-add (EPI_RESID), whole 128-byte rows either way.
+template <int MODE, int COLS>
+__device__ __forceinline__ void epi_sums(const Epi& ep, const CUtensorMap& tmX, float* tile, int lane, const float (&v)[COLS],
+                                         int row0, int n, int M) {
+  const bool gated = MODE == EPI_RESID && (ep.gate_a || ep.gate_b);
+  float4* row = reinterpret_cast<float4*>(tile + lane * 32);
+  auto vec = [&](const float* p, int i, float other) {
+    return p ? __ldg(reinterpret_cast<const float4*>(p + i)) : make_float4(other, other, other, other);
+  };
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) {
+    if (lane == 0) bulk_wait_group_read<0>();   // the copy that last read this tile is done with it
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = n + c + 4 * j;
+      const float4 b = vec(ep.bias, i, 0.f);
+      float4 x = make_float4(v[c + 4 * j] + b.x, v[c + 4 * j + 1] + b.y, v[c + 4 * j + 2] + b.z, v[c + 4 * j + 3] + b.w);
+      if (gated) {
+        const float4 ga = vec(ep.gate_a, i, 0.f), gb = vec(ep.gate_b, i, 0.f);
+        x = make_float4(x.x * (ga.x + gb.x), x.y * (ga.y + gb.y), x.z * (ga.z + gb.z), x.w * (ga.w + gb.w));
+      }
+      row[j ^ (lane & 7)] = x;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && row0 < M) {   // rows past M inside the box are skipped by the TMA
+      if (MODE == EPI_RESID) tma_reduce_add_2d(tile, &tmX, n + c, row0);
+      else tma_store_2d(tile, &tmX, n + c, row0);
+      bulk_commit_group();
+    }
+  }
+}
 
 template <int BN, int MODE, bool F8, typename X>
 __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmX,
                                           const Epi& ep, int M, int N, int K, const X& ex) {
   using C = Cfg<BN>;
+  constexpr int SUM = X::template sum_every<MODE>();
+  constexpr int STG = SUM > 0 ? 8 * 4096 : C::stg(MODE);   // staging: one 32 x 32 fp32 tile a warp, or the mode's
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + C::STAGES * C::A_BYTES;
   float* stg = reinterpret_cast<float*>(sB + C::STAGES * C::B_BYTES);   // 1024-byte aligned
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + C::STAGES * C::B_BYTES + C::stg(MODE));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + C::STAGES * C::B_BYTES + STG);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;   // [2]
   uint64_t* tempty = tfull + 2;          // [2]
@@ -271,7 +327,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 4 * epi_wg<MODE>()); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 4 * X::template wg<MODE>()); }
     mbar_init(tdone, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
@@ -335,10 +391,18 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, SITE_TEMPTY)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t d = tmem + acc * BN;
+        uint32_t d = tmem + acc * BN;
         [[maybe_unused]] typename X::Row row{};
         if constexpr (X::ON) { if (t != blockIdx.x) row = ex.row(t / n_tiles); }
         for (int k = 0; k < k_iters; ++k) {
+          if constexpr (SUM > 0) {
+            if (k && k % SUM == 0) {   // hand this part over and go on in the other accumulator
+              umma_commit(&tfull[acc]);
+              if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+              if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, SITE_TEMPTY)) { ok = false; break; }
+              d = tmem + acc * BN;
+            }
+          }
           if (!mbar_wait(&full[stage], phase, SITE_FULL)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_lo = a_lo0 + stage * (C::A_BYTES >> 4), b_lo = b_lo0 + stage * (C::B_BYTES >> 4);
@@ -347,7 +411,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
             if constexpr (F8)
               umma_ss_f8_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, C::IDESC_F8, (k | kk) != 0);
             else
-              umma_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, C::IDESC, (k | kk) != 0);
+              umma_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, C::IDESC, SUM ? (k % (SUM ? SUM : 1) | kk) != 0 : (k | kk) != 0);
           }
           umma_commit(&empty[stage]);   // frees the smem slot once these MMAs have read it
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
@@ -377,22 +441,40 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     __syncwarp();
   } else {
     // ---------------------------------------------------------- epilogue warps
-    constexpr int COLS = BN / epi_wg<MODE>();
+    constexpr int COLS = BN / X::template wg<MODE>();
     const int c_begin = ((warp - 2) >> 2) * COLS;
     int acc = 0;
     uint32_t acc_phase = 0;
     uint32_t chunk = 0;   // staging tiles used so far (alternating)
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const int m0 = (t / n_tiles) * BM, n0 = (t % n_tiles) * BN;
-      if (!mbar_wait_warp(&tfull[acc], acc_phase, SITE_TFULL)) break;
-      tc_fence_after();
-      epi_tile<BN, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN, m0, n0, M, chunk);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
-      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    if constexpr (SUM > 0) {
+      const int parts = (k_iters + SUM - 1) / SUM, q = warp & 3;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        float v[COLS];
+        for (int p = 0; p < parts; ++p) {
+          if (!mbar_wait_warp(&tfull[acc], acc_phase, SITE_TFULL)) { ok = false; break; }
+          tc_fence_after();
+          add_columns(tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + c_begin, v, p == 0);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc]);
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        }
+        if (ok) epi_sums<MODE>(ep, tmX, stg + (warp - 2) * 1024, lane, v, t / n_tiles * BM + q * 32, t % n_tiles * BN + c_begin, M);
+      }
+    } else {
+      for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int m0 = (t / n_tiles) * BM, n0 = (t % n_tiles) * BN;
+        if (!mbar_wait_warp(&tfull[acc], acc_phase, SITE_TFULL)) break;
+        tc_fence_after();
+        epi_tile<BN, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN, m0, n0, M, chunk);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[acc]);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
     }
-    if ((MODE == EPI_RESID || (staged2<MODE>() && COLS % 64 == 0)) && lane == 0)
+    if ((SUM > 0 || MODE == EPI_RESID || (staged2<MODE>() && COLS % 64 == 0)) && lane == 0)
       bulk_wait_group<0>();   // reductions and stores performed before exit
   }
 

@@ -543,8 +543,9 @@ size_t wd_gemm_lora_bytes(int M, int n_seg, int rank);
  * a the adapter of row m's request, then wd_gemm's epilogues (0, 1, 2, 3, 5) on v.
  * A [M, K], W [N, K] bf16 dense, N a multiple of 64, K a multiple of 8.  The
  * rank-wide middle A down^T is summed in fp32 and enters the second product
- * rounded to bf16 for 2-byte outputs, and as a sum of two bf16 parts (2^-17) for
- * fp32 outputs (epilogues 2 and 3).  ws: wd_gemm_lora_bytes(M, n_seg, rank)
+ * rounded to bf16 for 2-byte outputs, and as a sum of three bf16 parts (2^-26) for
+ * fp32 outputs (epilogues 2 and 3), whose accumulation is rounded to nearest
+ * every 512 of K instead of truncated throughout as in wd_gemm.  ws: wd_gemm_lora_bytes(M, n_seg, rank)
  * bytes, not shared with a call that may run at the same time.
  * Errors: N, K, rank, n_seg (1 .. 65536), n_adapters < 1, M above 2^29,
  * n_adapters*N above 2^31 - 1 -> WD_ERR_SHAPE; the workspace -> WD_ERR_WORKSPACE. */
