@@ -227,7 +227,8 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       bool ok = true;
       for (int index = blockIdx.x, n = 0; ok && index >= 0; ++round) {
         Work w;
-        if (find_work(p, index, lane, w)) {
+        const bool found = find_work(p, index, lane, w);
+        if (found) {
           const int nt = w.lq - w.l0 > BQ ? 2 : 1, l1 = min(w.l0 + NQ * BQ, w.lq);
           int n_hi = (w.lk + BK - 1) / BK;
           w.n_lo = 0;
@@ -296,15 +297,20 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
           }
           if (!ok) break;
         }
-        // the next pending block's work, asked for when this pair's loads are under way
-        if (lane == 0) {
-          mbar_arrive_expect_tx(asked, 16);
-          next_block_ask(answer, asked);
+        // The next pending block's work, asked for when this pair's loads are under way.  A block
+        // without a pair asks no more (there are such blocks behind the last pair, many of them where
+        // most of q lies outside the sequences): those still pending start and end by themselves.
+        index = -1;
+        if (found) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(asked, 16);
+            next_block_ask(answer, asked);
+          }
+          ok = mbar_wait_warp(asked, round & 1u, SITE_NEXT);
+          if (ok) index = next_block_answer(answer);
+          fence_proxy_async_smem();   // read before the next answer is written
+          __syncwarp();
         }
-        ok = mbar_wait_warp(asked, round & 1u, SITE_NEXT);
-        index = ok ? next_block_answer(answer) : -1;
-        fence_proxy_async_smem();   // read before the next answer is written
-        __syncwarp();
         if (index < 0 && ok) {      // the end, published like a pair
           ok = mbar_wait_warp(&work_empty[n & 1], ((n >> 1) & 1) ^ 1u, SITE_WORKE);
           if (lane == 0 && ok) {

@@ -42,7 +42,7 @@ wd_status wd_attention_packed(int dtype, int n_seq, int heads, int kv_heads, int
     return WD_ERR_DTYPE;
   }
   if (dh != 64 && dh != 128) { set_error("attention_packed: head dim %d (64 or 128)", dh); return WD_ERR_UNSUPPORTED; }
-  if (n_seq <= 0 || q_rows <= 0 || k_rows <= 0 || n_seq > MAX_ROWS || q_rows > MAX_ROWS || k_rows > MAX_ROWS) {
+  if (n_seq <= 0 || q_rows <= 0 || k_rows <= 0 || n_seq > 65536 || q_rows > MAX_ROWS || k_rows > MAX_ROWS) {
     set_error("attention_packed: n_seq=%d, q_rows=%lld, k_rows=%lld", n_seq, (long long)q_rows, (long long)k_rows);
     return WD_ERR_SHAPE;
   }
@@ -54,7 +54,7 @@ wd_status wd_attention_packed(int dtype, int n_seq, int heads, int kv_heads, int
     set_error("attention_packed: radius %d (1..%d with a bias, 0 without)", radius, pka::MAX_RADIUS);
     return WD_ERR_SHAPE;
   }
-  if (!positive(scale)) { set_error("attention_packed: scale %g", scale); return WD_ERR_ARG; }
+  if (!positive(scale) || !positive(scale * pka::LOG2E)) { set_error("attention_packed: scale %g", scale); return WD_ERR_ARG; }
   WD_TRY(check_stride("attention_packed q", q_rs, static_cast<int64_t>(heads) * dh));
   WD_TRY(check_stride("attention_packed k, v", kv_rs, static_cast<int64_t>(kv_heads) * dh));
   WD_TRY(check_stride("attention_packed o", o_rs, static_cast<int64_t>(heads) * dh));
@@ -163,7 +163,7 @@ wd_status wd_gemm_lora(int M, int N, int K, const void* A, const void* W, const 
     return WD_ERR_SHAPE;
   }
   const size_t need = wd_gemm_lora_bytes(M, lora->n_seg, lora->rank);
-  if (!need || lora->n_adapters <= 0 || static_cast<int64_t>(lora->n_adapters) * N > 0x7fffffff) {
+  if (!need || lora->n_adapters <= 0 || static_cast<int64_t>(lora->n_adapters) * (N > lora->rank ? N : lora->rank) > 0x7fffffff) {
     set_error("gemm_lora: n_seg=%d, n_adapters=%d, rank=%d (a multiple of 8 up to %d)", lora->n_seg, lora->n_adapters,
               lora->rank, lora::MAX_RANK);
     return WD_ERR_SHAPE;

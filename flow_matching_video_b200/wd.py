@@ -441,6 +441,8 @@ def wd_gemm_lora(M, N, K, A, W, bias, lora: wd_lora, epilogue, out, ws, gate_a=N
     for t in (bias, gate_a, gate_b):
         if t is not None:
             _take(f, t, f32, (N,))
+    if not hasattr(lora, "tensors"):
+        raise ValueError(f"{f}: a wd_lora made by wd_lora.of is wanted (it holds the tensors)")
     seg, adapter, down, up, scale = lora.tensors
     if down.shape[2] != K or up.shape[1] != N:
         raise ValueError(f"{f}: adapters of {up.shape[1]} x {down.shape[2]} for a layer of {N} x {K}")

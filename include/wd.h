@@ -465,7 +465,7 @@ wd_status wd_gemm_fp8(int M, int N, int K, const void* Aq, const float* sa, cons
  *   whatever they hold.
  * Errors: dh or dtype not above -> WD_ERR_UNSUPPORTED / WD_ERR_DTYPE; empty
  * shapes, heads not a multiple of kv_heads, strides below the width, more than
- * 2^30 rows, radius out of range -> WD_ERR_SHAPE; scale not finite and positive
+ * 2^30 rows or 65536 sequences, radius out of range -> WD_ERR_SHAPE; scale not finite and positive
  * -> WD_ERR_ARG; strides not multiples of 8 -> WD_ERR_ALIGN. */
 wd_status wd_attention_packed(int dtype, int n_seq, int heads, int kv_heads, int dh, const void* q, int64_t q_rs,
                               int64_t q_rows, const int* cu_q, const void* k, const void* v, int64_t kv_rs,
@@ -548,7 +548,7 @@ size_t wd_gemm_lora_bytes(int M, int n_seg, int rank);
  * every 512 of K instead of truncated throughout as in wd_gemm.  ws: wd_gemm_lora_bytes(M, n_seg, rank)
  * bytes, not shared with a call that may run at the same time.
  * Errors: N, K, rank, n_seg (1 .. 65536), n_adapters < 1, M above 2^29,
- * n_adapters*N above 2^31 - 1 -> WD_ERR_SHAPE; the workspace -> WD_ERR_WORKSPACE. */
+ * n_adapters * max(N, rank) above 2^31 - 1 -> WD_ERR_SHAPE; the workspace -> WD_ERR_WORKSPACE. */
 wd_status wd_gemm_lora(int M, int N, int K, const void* A, const void* W, const float* bias, const wd_lora* lora,
                        int epilogue, void* out, const float* gate_a, const float* gate_b, void* ws, size_t ws_bytes,
                        wd_stream stream);

@@ -764,3 +764,17 @@ def test_gemm_lora_sm_pairs(wd, epi, M, N, K, rank):
     of a tile, lie in one half only, or cover several tiles; rows of none at both ends."""
     lens = [1, 127, 128, 200, 3, 0, 56, 600, 5000, 130, 126, 1, 9000]
     run_lora(wd, lens, [0, 1, 2, -1, 1, 0, 2, 0, 1, 2, 0, 1, 0], M, N, K, rank, 3, epi, start=70)
+
+
+def test_attention_packed_mostly_spare_rows(wd):
+    """A large buffer with few rows in use: most blocks of the grid find nothing."""
+    g = gen(22)
+    q = torch.zeros((3_000_000, 64), dtype=torch.bfloat16, device="cuda")
+    q[500:900] = normal(g, (400, 64), torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    cu = ints([500, 600, 600, 900])
+    wd.wd_attention_packed(wd.WD_BF16, 1, 1, 64, q, q, q, cu, cu, 0.125, out)
+    wd.wd_check()
+    want, ab = attention64(q[500:900], q[500:900], q[500:900], [0, 100, 100, 400], [0, 100, 100, 400], 1, 1, 64, 0.125)
+    assert_within(out[500:900], want, attention_bound(want, ab, torch.bfloat16, 300, q[500:900]))
+    assert (out[:500] == 7.0).all() and (out[900:] == 7.0).all()

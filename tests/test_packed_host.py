@@ -30,11 +30,11 @@ def attention(wd, **kw):
     (ALIGN, dict(q=Q + 8)), (ALIGN, dict(o=O + 4)), (ALIGN, dict(cu_k=CU + 4)), (ALIGN, dict(bias=B + 4, radius=3)),
     (DTYPE, dict(dtype=0)), (DTYPE, dict(dtype=3)), (DTYPE, dict(dtype=9)),
     (UNSUPPORTED, dict(dh=32)), (UNSUPPORTED, dict(dh=256)), (UNSUPPORTED, dict(dh=0)),
-    (SHAPE, dict(n_seq=0)), (SHAPE, dict(q_rows=0)), (SHAPE, dict(k_rows=0)), (SHAPE, dict(k_rows=(1 << 30) + 1)),
+    (SHAPE, dict(n_seq=0)), (SHAPE, dict(n_seq=65537)), (SHAPE, dict(q_rows=0)), (SHAPE, dict(k_rows=0)), (SHAPE, dict(k_rows=(1 << 30) + 1)),
     (SHAPE, dict(heads=0)), (SHAPE, dict(heads=5)), (SHAPE, dict(kv_heads=0)), (SHAPE, dict(kv_heads=3)),
     (SHAPE, dict(heads=65536, kv_heads=1)),
     (SHAPE, dict(radius=4)), (SHAPE, dict(bias=B)), (SHAPE, dict(bias=B, radius=1025)), (SHAPE, dict(bias=B, radius=-1)),
-    (ARG, dict(scale=0.0)), (ARG, dict(scale=-1.0)), (ARG, dict(scale=math.nan)), (ARG, dict(scale=math.inf)),
+    (ARG, dict(scale=0.0)), (ARG, dict(scale=-1.0)), (ARG, dict(scale=math.nan)), (ARG, dict(scale=math.inf)), (ARG, dict(scale=3e38)),
     (SHAPE, dict(q_rs=504)), (SHAPE, dict(kv_rs=248)), (SHAPE, dict(o_rs=0)), (ALIGN, dict(q_rs=516)), (ALIGN, dict(kv_rs=257)),
 ], ids=str)
 def test_attention_packed_refusals(wd, want, kw):
@@ -94,7 +94,7 @@ def lora(wd, n_seg=2, n_adapters=3, rank=16, seg=CU, adapter=CU, down=K, up=V, s
     (ARG, dict(epilogue=4)), (ARG, dict(epilogue=6)), (ARG, dict(epilogue=-1)),
     (SHAPE, dict(M=0)), (SHAPE, dict(N=0)), (SHAPE, dict(N=96)), (SHAPE, dict(K=0)), (SHAPE, dict(K=12)), (SHAPE, dict(M=(1 << 29) + 1)),
     (SHAPE, dict(rank=0)), (SHAPE, dict(rank=12)), (SHAPE, dict(rank=264)), (SHAPE, dict(n_seg=0)), (SHAPE, dict(n_seg=65537)),
-    (SHAPE, dict(n_adapters=0)), (SHAPE, dict(n_adapters=1 << 24)), (WORKSPACE, dict(ws_bytes=1000)), (WORKSPACE, dict(M=3000)),
+    (SHAPE, dict(n_adapters=0)), (SHAPE, dict(n_adapters=1 << 24)), (SHAPE, dict(N=64, n_adapters=1 << 25, rank=256)), (WORKSPACE, dict(ws_bytes=1000)), (WORKSPACE, dict(M=3000)),
 ], ids=str)
 def test_gemm_lora_refusals(wd, want, kw):
     assert lora(wd, **kw) == want
@@ -151,5 +151,7 @@ def test_binding_checks_tensors_against_the_sizes(wd):
         wd.wd_gemm_lora(9, 256, 128, A, W, None, ld, 0, out, ws)
     with pytest.raises(ValueError, match="(?!.*one CUDA device)"):
         wd.wd_gemm_lora(9, 256, 128, A, W, None, ld, 2, out, ws)
+    with pytest.raises(ValueError, match="wd_lora.of"):
+        wd.wd_gemm_lora(9, 256, 128, A, W, None, wd.wd_lora(1, 1, 8, 0, 0, 0, 0, 0), 0, out, ws)
     with pytest.raises(ValueError, match="adapters of 256 x 128"):
         wd.wd_gemm_lora(9, 256, 64, A[:, :64].contiguous(), W[:, :64].contiguous(), None, ld, 0, out, ws)
