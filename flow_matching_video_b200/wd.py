@@ -79,12 +79,12 @@ class wd_lora(C.Structure):
         na, r, k = _dims(down, 3, "down")
         n = _dims(up, 3, "up")[1]
         ns = adapter.numel()
-        _take(f, seg, _torch_type(f, "i32"), (ns + 1,))
-        _take(f, adapter, _torch_type(f, "i32"), (ns,))
-        _take(f, down, _torch_type(f, WD_BF16), (na, r, k))
-        _take(f, up, _torch_type(f, WD_BF16), (na, n, r))
-        if scale is not None:
-            _take(f, scale, _torch_type(f, WD_F32), (na,))
+        i32, bf16 = _torch_type(f, "i32"), _torch_types[WD_BF16]
+        _take(f, i32, (ns + 1,), seg)
+        _take(f, i32, (ns,), adapter)
+        _take(f, bf16, (na, r, k), down)
+        _take(f, bf16, (na, n, r), up)
+        _take(f, _torch_types[WD_F32], (na,), scale)
         out = cls(ns, na, r, _p(seg), _p(adapter), _p(down), _p(up), _p(scale))
         out.tensors = (seg, adapter, down, up, scale)
         return out
@@ -173,11 +173,12 @@ def _dims(t, n, name):
     return t.shape
 
 
-def _take(where, t, dtype, shape):
-    """A dense tensor of this element type and shape."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{where}: a dense {dtype} tensor {list(shape)} is wanted, not {t.dtype} {list(t.shape)}"
-                         f" with strides {list(t.stride())}")
+def _take(where, dtype, shape, *tensors):
+    """Dense tensors (or None) of this element type and shape."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{where}: a dense {dtype} tensor {list(shape)} is wanted, not {t.dtype} {list(t.shape)}"
+                             f" with strides {list(t.stride())}")
 
 
 def _rows(where, t, dtype, width, rows=None):
@@ -207,13 +208,23 @@ def _torch_type(where, dtype):
         raise ValueError(f"{where}: dtype {dtype}") from None
 
 
-def _launch(where, tensors, stream, call, *args):
-    """call(*args, stream handle) on the tensors' own device: its current stream, or the one given."""
+def _pointers(where, *tensors):
+    """The device they share, and their addresses (None stays None)."""
     dev = tensors[0].get_device()
+    out = []
     for t in tensors:
-        if t is not None and (dev < 0 or t.get_device() != dev):
-            raise ValueError(f"{where}: tensors on {sorted({str(t.device) for t in tensors if t is not None})}, one CUDA"
+        if t is None:
+            out.append(None)
+        elif dev < 0 or t.get_device() != dev:
+            raise ValueError(f"{where}: tensors on {sorted({str(x.device) for x in tensors if x is not None})}, one CUDA"
                              " device is wanted")
+        else:
+            out.append(t.data_ptr())
+    return dev, out
+
+
+def _launch(where, dev, stream, call, *args):
+    """call(*args, stream handle) on device dev: its current stream, or the one given."""
     # the stream's handle without a Stream object: 0.1 us instead of 3
     st = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
     if _torch.cuda.current_device() == dev:
@@ -360,21 +371,21 @@ def wd_attention_packed(dtype, heads, kv_heads, dh, q, k, v, cu_q, cu_k, scale, 
     """q, o [q_rows, heads*dh], k, v [k_rows, kv_heads*dh] (row strides may differ, k and v
     share theirs), cu_q, cu_k int32 [n_seq + 1], bias fp32 [heads, 2 radius + 1] or None."""
     f = "wd_attention_packed"
-    td, i32 = _torch_type(f, dtype), _torch_types["i32"]
-    q_rs, k_rs, v_rs = _rows(f, q, td, heads * dh), _rows(f, k, td, kv_heads * dh), _rows(f, v, td, kv_heads * dh, k.shape[0])
-    o_rs = _rows(f, o, _torch_types[WD_BF16], heads * dh, q.shape[0])
+    td = _torch_type(f, dtype)
+    wq, wk = heads * dh, kv_heads * dh
+    q_rs, k_rs, v_rs = _rows(f, q, td, wq), _rows(f, k, td, wk), _rows(f, v, td, wk, k.shape[0])
+    o_rs = _rows(f, o, _torch_types[WD_BF16], wq, q.shape[0])
     if k_rs != v_rs:
         raise ValueError(f"{f}: row strides {k_rs} of k and {v_rs} of v")
     n_seq = cu_q.numel() - 1
-    _take(f, cu_q, i32, (n_seq + 1,))
-    _take(f, cu_k, i32, (n_seq + 1,))
+    _take(f, _torch_types["i32"], (n_seq + 1,), cu_q, cu_k)
     radius = 0
     if bias is not None:
         radius = (_dims(bias, 2, "bias")[1] - 1) // 2
-        _take(f, bias, _torch_types[WD_F32], (heads, 2 * radius + 1))
-    _launch(f, (q, k, v, cu_q, cu_k, o, bias), stream, _lib.wd_attention_packed,
-            dtype, n_seq, heads, kv_heads, dh, _p(q), q_rs, q.shape[0], _p(cu_q), _p(k), _p(v), k_rs, k.shape[0], _p(cu_k),
-            scale, _p(bias), radius, _p(o), o_rs)
+        _take(f, _torch_types[WD_F32], (heads, 2 * radius + 1), bias)
+    dev, (q_, k_, v_, cq_, ck_, o_, b_) = _pointers(f, q, k, v, cu_q, cu_k, o, bias)
+    _launch(f, dev, stream, _lib.wd_attention_packed, dtype, n_seq, heads, kv_heads, dh, q_, q_rs, q.shape[0], cq_, k_, v_,
+            k_rs, k.shape[0], ck_, scale, b_, radius, o_, o_rs)
 
 
 def wd_qknorm_rope_axes(dtype, dh, axes: wd_rope_axes, pos, q, g_q, q_out, k=None, g_k=None, k_out=None, eps=1e-6,
@@ -393,14 +404,12 @@ def wd_qknorm_rope_axes(dtype, dh, axes: wd_rope_axes, pos, q, g_q, q_out, k=Non
             ko_rs = _rows(f, k_out, td, wk, rows)
     if (k is None) != (k_out is None) or dh <= 0 or wq % dh or wk % dh:
         raise ValueError(f"{f}: rows of {wq} and {wk} elements with heads of {dh}; k and k_out go together")
-    _take(f, pos, _torch_types["i32"], (rows, 3))
-    if g_q is not None:
-        _take(f, g_q, f32, (wq,))
-    if g_k is not None:
-        _take(f, g_k, f32, (wk,))
-    _launch(f, (q, q_out, pos, k, k_out, g_q, g_k), stream, _lib.wd_qknorm_rope_axes,
-            dtype, rows, dh, C.byref(axes), _p(pos), _p(q), q_rs, wq // dh, _p(g_q), _p(q_out), qo_rs, _p(k), k_rs, wk // dh,
-            _p(g_k), _p(k_out), ko_rs, eps)
+    _take(f, _torch_types["i32"], (rows, 3), pos)
+    _take(f, f32, (wq,), g_q)
+    _take(f, f32, (wk,), g_k)
+    dev, (q_, qo_, p_, k_, ko_, gq_, gk_) = _pointers(f, q, q_out, pos, k, k_out, g_q, g_k)
+    _launch(f, dev, stream, _lib.wd_qknorm_rope_axes, dtype, rows, dh, axes, p_, q_, q_rs, wq // dh, gq_, qo_, qo_rs, k_, k_rs,
+            wk // dh, gk_, ko_, ko_rs, eps)
 
 
 def wd_add_norm(x_dtype, x, y_dtype, y, norm, gain, beta, eps, sum, out_dtype, out, scale=None, stream=None):
@@ -409,20 +418,14 @@ def wd_add_norm(x_dtype, x, y_dtype, y, norm, gain, beta, eps, sum, out_dtype, o
     f = "wd_add_norm"
     tx, f32 = _torch_type(f, x_dtype), _torch_types[WD_F32]
     shape = rows, D = _dims(x, 2, "x")
-    _take(f, x, tx, shape)
+    _take(f, tx, shape, x, sum)
     if y is not None:
-        _take(f, y, _torch_type(f, y_dtype), shape)
-    if sum is not None:
-        _take(f, sum, tx, shape)
-    _take(f, out, _torch_type(f, out_dtype), shape)
-    if gain is not None:
-        _take(f, gain, f32, (D,))
-    if beta is not None:
-        _take(f, beta, f32, (D,))
-    if scale is not None:
-        _take(f, scale, f32, (rows,))
-    _launch(f, (x, y, gain, beta, sum, out, scale), stream, _lib.wd_add_norm,
-            rows, D, x_dtype, _p(x), y_dtype, _p(y), norm, _p(gain), _p(beta), eps, _p(sum), out_dtype, _p(out), _p(scale))
+        _take(f, _torch_type(f, y_dtype), shape, y)
+    _take(f, _torch_type(f, out_dtype), shape, out)
+    _take(f, f32, (D,), gain, beta)
+    _take(f, f32, (rows,), scale)
+    dev, (x_, y_, g_, b_, s_, o_, sc_) = _pointers(f, x, y, gain, beta, sum, out, scale)
+    _launch(f, dev, stream, _lib.wd_add_norm, rows, D, x_dtype, x_, y_dtype, y_, norm, g_, b_, eps, s_, out_dtype, o_, sc_)
 
 
 def wd_gemm_lora_bytes(M: int, n_seg: int, rank: int) -> int:
@@ -434,20 +437,18 @@ def wd_gemm_lora(M, N, K, A, W, bias, lora: wd_lora, epilogue, out, ws, gate_a=N
     [M, N] in the epilogue's type, ws at least wd_gemm_lora_bytes bytes."""
     f = "wd_gemm_lora"
     bf16, f32 = _torch_type(f, WD_BF16), _torch_types[WD_F32]
-    _take(f, A, bf16, (M, K))
-    _take(f, W, bf16, (N, K))
-    _take(f, out, f32 if epilogue in (EPI_F32, EPI_RESID) else _torch_types[WD_F16] if epilogue == EPI_STORE_F16 else bf16,
-          (M, N))
-    for t in (bias, gate_a, gate_b):
-        if t is not None:
-            _take(f, t, f32, (N,))
+    _take(f, bf16, (M, K), A)
+    _take(f, bf16, (N, K), W)
+    _take(f, f32 if epilogue in (EPI_F32, EPI_RESID) else _torch_types[WD_F16] if epilogue == EPI_STORE_F16 else bf16,
+          (M, N), out)
+    _take(f, f32, (N,), bias, gate_a, gate_b)
     if not hasattr(lora, "tensors"):
         raise ValueError(f"{f}: a wd_lora made by wd_lora.of is wanted (it holds the tensors)")
-    seg, adapter, down, up, scale = lora.tensors
+    down, up = lora.tensors[2:4]
     if down.shape[2] != K or up.shape[1] != N:
         raise ValueError(f"{f}: adapters of {up.shape[1]} x {down.shape[2]} for a layer of {N} x {K}")
-    _launch(f, (A, W, bias, gate_a, gate_b, out, ws, seg, adapter, down, up, scale), stream, _lib.wd_gemm_lora,
-            M, N, K, _p(A), _p(W), _p(bias), C.byref(lora), epilogue, _p(out), _p(gate_a), _p(gate_b), _p(ws), ws.nbytes)
+    dev, (a_, w_, b_, ga_, gb_, o_, ws_, *_) = _pointers(f, A, W, bias, gate_a, gate_b, out, ws, *lora.tensors)
+    _launch(f, dev, stream, _lib.wd_gemm_lora, M, N, K, a_, w_, b_, lora, epilogue, o_, ga_, gb_, ws_, ws.nbytes)
 
 
 def wd_test_exp2(x, y_fma, y_fma2, y_mufu, y_lib, stream=None):
