@@ -26,6 +26,12 @@
 // repeated 160 times so that no index needs clamping; a block of keys that lies R
 // or further from all of a warp's rows takes the one end value instead.  Where an
 // end value is -inf, key blocks wholly behind it are neither loaded nor multiplied.
+//
+// Bound: per 128-key block of a pair the softmax's instructions (about 700 a warp, two warps a
+// sub-partition) take as long as the MMAs of 128-wide heads, and longer than those of 64-wide ones;
+// in a sustained loop the power cap holds both down.  Measured (B200): 7800 + 32760 tokens x 12 heads of 128
+// 5.9 - 6.2 ms (1120 - 1180 TFLOP/s; k_attn_tc on the two sequences one after the other 6.2 - 6.4 ms), 7800 +
+// 3185 + 405 tokens 0.37 - 0.43 ms, 43746 rows to 512 / 77 / 9 / 0 keys 0.127 - 0.149 ms.
 #include "wd_internal.cuh"
 
 namespace wd {
@@ -35,7 +41,9 @@ constexpr int BQ = 128, BK = 128, NQ = 2;
 constexpr int MAX_RADIUS = 1024, PAD = 160;   // PAD >= 127 + 31 + 1: a tile's reach past +-R
 constexpr float LOG2E = 1.4426950408889634f;
 // Warps: 0 loads, 1 issues MMAs, 2 and 3 only fill their warpgroup, 4-7 and 8-11 are the
-// softmax warps of the tiles.  The first warpgroup hands most of its registers on.
+// softmax warps of the tiles.  The first warpgroup hands registers on to the softmax, whose thread
+// holds a row of 128 scores: 120 and 192 a thread took 6.0 - 6.1 ms for 32760 tokens x 12 heads, 56 and 224
+// 6.4 - 6.7 (the issuing thread then recomputes its descriptors), 136 and 184 6.4 - 6.6, 168 each 6.9.
 constexpr int THREADS = 384, REGS_FEW = 120, REGS_MANY = 192;
 static_assert(128 * (REGS_FEW + 2 * REGS_MANY) <= THREADS * 168, "registers of the block at launch");
 
@@ -252,7 +260,8 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
           auto load = [&](const CUtensorMap* tm, int row, uint64_t* bar) {
             uint8_t* dst = smem + C::RING_OFF + (pos % RING) * C::KV_BYTES;
             mbar_arrive_expect_tx(bar, C::KV_BYTES);
-            for (int hf = 0; hf < C::HALVES; ++hf) tma_load_3d(dst + hf * C::HALF_BYTES, tm, kvc + hf * 64, row, 0, bar);
+            for (int hf = 0; hf < C::HALVES; ++hf)
+              tma_load_3d(dst + hf * C::HALF_BYTES, tm, kvc + hf * 64, row, 0, bar);
           };
           if (w.nb && lane == 0) {
             for (int t = 0; t < nt && ok; ++t) {
@@ -298,17 +307,19 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
           if (!ok) break;
         }
         // The next pending block's work: early enough to have the next pair's loads under way when
-        // this one ends, and late enough to leave the work to blocks that are free sooner.  With
-        // a ring of two key blocks (128-wide heads) the loads end two blocks before the pair; with
-        // four (64-wide heads) a short sequence's would end at its start, so the K tile of the last
-        // block but one has to be used first (two prompts of 512 and 77 tokens x 64 heads: 20.2 -> 18.5
-        // us; 128-wide heads lost 2 % by the same).  A block without a pair
-        // asks no more (there are such blocks behind the last pair, many of them where most of q
-        // lies outside the sequences): those still pending start and end by themselves.
+        // this one ends, and late enough to leave the work to blocks that are free sooner.  With a
+        // ring of two key blocks (128-wide heads) the loads end two blocks before the pair; with four
+        // (64-wide heads) a short sequence's would end at its start, so the K tile of the last block
+        // but one has to be used first (prompts of 512 and 77 tokens x 64 heads: 20.2 -> 18.5 us;
+        // 128-wide heads lost 2 % by the same).  A block without a pair asks no more (there are
+        // such blocks behind the last pair, many of them where most of q lies outside the
+        // sequences): those still pending start and end by themselves.
         index = -1;
         if (found) {
-          if (RING > 4 && w.nb >= 2) ok = mbar_wait_warp(&kv_empty[(pos - 4) % RING], ((pos - 4) / RING) & 1u, SITE_NEXT);
-          if (!ok) break;
+          if (RING > 4 && w.nb >= 2) {
+            ok = mbar_wait_warp(&kv_empty[(pos - 4) % RING], ((pos - 4) / RING) & 1u, SITE_NEXT);
+            if (!ok) break;
+          }
           if (lane == 0) {
             mbar_arrive_expect_tx(asked, 16);
             next_block_ask(answer, asked);
@@ -341,7 +352,8 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const uint32_t r0 = smem_u32(smem + C::RING_OFF);
         const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::Q_OFF), 16, 1024), dk0 = sdesc_sw128(r0, 16, 1024);
         const uint64_t dv0 = sdesc_sw128(r0, C::HALF_BYTES, 1024);
-        const uint32_t q_lo = static_cast<uint32_t>(dq0), k_lo = static_cast<uint32_t>(dk0), v_lo = static_cast<uint32_t>(dv0);
+        const uint32_t q_lo = static_cast<uint32_t>(dq0), k_lo = static_cast<uint32_t>(dk0);
+        const uint32_t v_lo = static_cast<uint32_t>(dv0);
         const uint32_t s_hi = static_cast<uint32_t>(dq0 >> 32), v_hi = static_cast<uint32_t>(dv0 >> 32);
         uint32_t u = 0;                   // key blocks so far: K of block u is ring position 2u, V 2u + 1
         uint32_t blocks[NQ] = {0, 0};     // key blocks of each tile before this pair
@@ -447,7 +459,8 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             return mbar_wait_warp(tab_bar, tabs++ & 1u, SITE_TAB);
           };
           if (!all_softmax_warps()) break;           // the old table has been used
-          for (int i = threadIdx.x - 128; i < 2 * (R + PAD) + 1; i += 256) tab[i] = log2_units(tb[min(max(i - PAD, 0), 2 * R)]);
+          for (int i = threadIdx.x - 128; i < 2 * (R + PAD) + 1; i += 256)
+            tab[i] = log2_units(tb[min(max(i - PAD, 0), 2 * R)]);
           if (!all_softmax_warps()) break;
           tab_h = w.h;
         }
@@ -458,7 +471,8 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         continue;
       }
       const int keys = w.lk - w.n_lo * BK;                               // from the first key block on
-      [[maybe_unused]] const int far = w.n_lo * BK - (w.l0 + t * BQ + quarter * 32);   // its first key, from the warp's first row
+      // that block's first key, counted from the warp's first row
+      [[maybe_unused]] const int far = w.n_lo * BK - (w.l0 + t * BQ + quarter * 32);
       float m = -INFINITY, l = 0.f;
       for (int n = 0; n < nb; ++n) {
         if (!mbar_wait_warp(&s_full[t], blocks & 1u, SITE_S)) { ok = false; break; }
@@ -646,9 +660,10 @@ static wd_status attention_packed_t(int dh, int kv_heads, const void* q, int64_t
   WD_TRY(make_tmap_rows(&tq, ty, q, p.q_rows, static_cast<int64_t>(p.heads) * dh, q_rs));
   WD_TRY(make_tmap_rows(&tk, ty, k, p.k_rows, static_cast<int64_t>(kv_heads) * dh, kv_rs));
   WD_TRY(make_tmap_rows(&tv, ty, v, p.k_rows, static_cast<int64_t>(kv_heads) * dh, kv_rs));
-  if (dh == 128)
-    return p.bias ? launch_attn_packed<128, TI, true>(tq, tk, tv, p, st) : launch_attn_packed<128, TI, false>(tq, tk, tv, p, st);
-  return p.bias ? launch_attn_packed<64, TI, true>(tq, tk, tv, p, st) : launch_attn_packed<64, TI, false>(tq, tk, tv, p, st);
+  if (dh == 128 && p.bias) return launch_attn_packed<128, TI, true>(tq, tk, tv, p, st);
+  if (dh == 128) return launch_attn_packed<128, TI, false>(tq, tk, tv, p, st);
+  if (p.bias) return launch_attn_packed<64, TI, true>(tq, tk, tv, p, st);
+  return launch_attn_packed<64, TI, false>(tq, tk, tv, p, st);
 }
 
 }  // namespace wd

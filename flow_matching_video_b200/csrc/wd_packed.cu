@@ -54,7 +54,10 @@ wd_status wd_attention_packed(int dtype, int n_seq, int heads, int kv_heads, int
     set_error("attention_packed: radius %d (1..%d with a bias, 0 without)", radius, pka::MAX_RADIUS);
     return WD_ERR_SHAPE;
   }
-  if (!positive(scale) || !positive(scale * pka::LOG2E)) { set_error("attention_packed: scale %g", scale); return WD_ERR_ARG; }
+  if (!positive(scale) || !positive(scale * pka::LOG2E)) {
+    set_error("attention_packed: scale %g", scale);
+    return WD_ERR_ARG;
+  }
   WD_TRY(check_stride("attention_packed q", q_rs, static_cast<int64_t>(heads) * dh));
   WD_TRY(check_stride("attention_packed k, v", kv_rs, static_cast<int64_t>(kv_heads) * dh));
   WD_TRY(check_stride("attention_packed o", o_rs, static_cast<int64_t>(heads) * dh));
@@ -77,14 +80,20 @@ wd_status wd_qknorm_rope_axes(int dtype, int64_t rows, int dh, const wd_rope_axe
   if (!axes) { set_error("%s: axes is NULL", __func__); return WD_ERR_ARG; }
   WD_NEED(pos); WD_NEED(q); WD_NEED(q_out); WD_OPT(g_q);
   if (k) { WD_NEED(k); WD_NEED(k_out); WD_OPT(g_k); }
-  if (dtype != WD_BF16 && dtype != WD_F32 && dtype != WD_F16) { set_error("qknorm_rope_axes: dtype %d", dtype); return WD_ERR_DTYPE; }
+  if (dtype != WD_BF16 && dtype != WD_F32 && dtype != WD_F16) {
+    set_error("qknorm_rope_axes: dtype %d", dtype);
+    return WD_ERR_DTYPE;
+  }
   if (rows <= 0 || rows > MAX_ROWS || dh < 8 || dh > 2 * rows::MAX_PAIRS || dh % 8) {
     set_error("qknorm_rope_axes: rows=%lld, dh=%d (a multiple of 8 in 8..%d)", (long long)rows, dh, 2 * rows::MAX_PAIRS);
     return WD_ERR_SHAPE;
   }
   int sum = 0;
   for (int i = 0; i < 3; ++i) {
-    if (axes->sec[i] < 0 || axes->sec[i] % 2 || axes->sec[i] > dh) { set_error("qknorm_rope_axes: section of %d channels", axes->sec[i]); return WD_ERR_SHAPE; }
+    if (axes->sec[i] < 0 || axes->sec[i] % 2 || axes->sec[i] > dh) {
+      set_error("qknorm_rope_axes: section of %d channels", axes->sec[i]);
+      return WD_ERR_SHAPE;
+    }
     sum += axes->sec[i];
   }
   if (sum != dh) { set_error("qknorm_rope_axes: sections add up to %d, not dh=%d", sum, dh); return WD_ERR_SHAPE; }
@@ -100,7 +109,10 @@ wd_status wd_qknorm_rope_axes(int dtype, int64_t rows, int dh, const wd_rope_axe
   a.in[1] = k; a.out[1] = k_out; a.gain[1] = g_k; a.in_rs[1] = k_rs; a.out_rs[1] = ko_rs;
   for (int i = 0; i < (k ? 2 : 1); ++i) {
     const int64_t n = i ? kv_heads : heads;
-    if (n <= 0 || n * dh > rows::ROW_MAX) { set_error("qknorm_rope_axes: %lld heads of %d (rows up to %d wide)", (long long)n, dh, rows::ROW_MAX); return WD_ERR_SHAPE; }
+    if (n <= 0 || n * dh > rows::ROW_MAX) {
+      set_error("qknorm_rope_axes: %lld heads of %d (rows up to %d wide)", (long long)n, dh, rows::ROW_MAX);
+      return WD_ERR_SHAPE;
+    }
     a.D[i] = static_cast<int>(n) * dh;
     a.inv_D[i] = 1.f / a.D[i];
     WD_TRY(check_stride(i ? "qknorm_rope_axes k" : "qknorm_rope_axes q", a.in_rs[i], a.D[i]));
@@ -157,13 +169,17 @@ wd_status wd_gemm_lora(int M, int N, int K, const void* A, const void* W, const 
   WD_NEED(A); WD_NEED(W); WD_OPT(bias); WD_NEED(out); WD_OPT(gate_a); WD_OPT(gate_b); WD_NEED(ws);
   if (!lora) { set_error("%s: lora is NULL", __func__); return WD_ERR_ARG; }
   WD_NEED(lora->seg); WD_NEED(lora->adapter); WD_NEED(lora->down); WD_NEED(lora->up); WD_OPT(lora->scale);
-  if (epilogue < 0 || epilogue > EPI_STORE_F16 || epilogue == EPI_UNPATCH) { set_error("gemm_lora: epilogue %d", epilogue); return WD_ERR_ARG; }
+  if (epilogue < 0 || epilogue > EPI_STORE_F16 || epilogue == EPI_UNPATCH) {
+    set_error("gemm_lora: epilogue %d", epilogue);
+    return WD_ERR_ARG;
+  }
   if (M <= 0 || M > (1 << 29) || N <= 0 || N % 64 || K <= 0 || K % 8) {
     set_error("gemm_lora: %d x %d x %d (N a multiple of 64, K of 8)", M, N, K);
     return WD_ERR_SHAPE;
   }
   const size_t need = wd_gemm_lora_bytes(M, lora->n_seg, lora->rank);
-  if (!need || lora->n_adapters <= 0 || static_cast<int64_t>(lora->n_adapters) * (N > lora->rank ? N : lora->rank) > 0x7fffffff) {
+  const int64_t most = N > lora->rank ? N : lora->rank;   // rows of up or down an adapter has
+  if (!need || lora->n_adapters <= 0 || lora->n_adapters * most > 0x7fffffff) {
     set_error("gemm_lora: n_seg=%d, n_adapters=%d, rank=%d (a multiple of 8 up to %d)", lora->n_seg, lora->n_adapters,
               lora->rank, lora::MAX_RANK);
     return WD_ERR_SHAPE;

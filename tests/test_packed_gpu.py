@@ -778,3 +778,17 @@ def test_attention_packed_mostly_spare_rows(wd):
     want, ab = attention64(q[500:900], q[500:900], q[500:900], [0, 100, 100, 400], [0, 100, 100, 400], 1, 1, 64, 0.125)
     assert_within(out[500:900], want, attention_bound(want, ab, torch.bfloat16, 300, q[500:900]))
     assert (out[:500] == 7.0).all() and (out[900:] == 7.0).all()
+
+
+def test_gemm_lora_long_sums_with_many_rows(wd):
+    """The same where the rows alone would not split K: an adapter that outweighs the rest."""
+    g = gen(15)
+    M, N, K, r = 20000, 256, 8960, 32
+    A, W = normal(g, (M, K), torch.bfloat16), normal(g, (N, K), torch.bfloat16, 0.002)
+    down, up = normal(g, (1, r, K), torch.bfloat16, K ** -0.5), normal(g, (1, N, r), torch.bfloat16)
+    out = torch.empty((M, N), device="cuda")
+    ws = torch.empty(wd.wd_gemm_lora_bytes(M, 1, r), dtype=torch.uint8, device="cuda")
+    wd.wd_gemm_lora(M, N, K, A, W, None, wd.wd_lora.of(ints([0, M]), ints([0]), down, up), wd.EPI_F32, out, ws)
+    wd.wd_check()
+    want = A[:2000].double() @ (W.double() + up[0].double() @ down[0].double()).t()
+    assert float(((out[:2000].double() - want).pow(2).mean() / want.pow(2).mean()).sqrt()) <= 3e-6
