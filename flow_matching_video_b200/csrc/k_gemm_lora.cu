@@ -616,12 +616,13 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   while (cols < static_cast<uint32_t>(rn)) cols *= 2;
   WD_TRY((allow_smem<lora::k_lora_down>(lora::smem_bytes(lora::MAX_RANK))));
   {
-    // enough blocks to fill the SMs twice over, with 4 stages of K each at least; for fp32 outputs
-    // also no more than 24 stages each, since a block's accumulator truncates (see sum_every)
+    // a block for every SM, with 4 stages of K each at least (258 blocks of 24 stages: 25 us, 516 of 12: 31);
+    // for fp32 outputs also no more than 24 stages each, since a block's accumulator truncates (see
+    // sum_every)
     int split = 1;
     const int k_iters = (K + lora::BK - 1) / lora::BK;
     const int64_t blocks = slabs * (a.tile / lora::BM);
-    while (split < lora::MAX_SPLIT && blocks * split < 2 * sm_count() && k_iters >= 8 * split) split *= 2;
+    while (split < lora::MAX_SPLIT && blocks * split < sm_count() && k_iters >= 8 * split) split *= 2;
     while (split < lora::MAX_SPLIT && a.parts > 1 && k_iters > 24 * split) split *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * split));

@@ -32,7 +32,8 @@ L, D, H, F, NI, NT = 32760, 1536, 12, 8960, 257, 512
 
 CASES = ("attn_self", "attn_cross", "attn_fp8", "attn_fp8_quantize", "gemm_qkv", "gemm_o", "gemm_ffn1", "gemm_ffn2",
          "gemm_ffn1_store", "euler", "euler_hbm", "gemm_fp8_qkv", "gemm_fp8_o", "gemm_fp8_ffn1", "gemm_fp8_ffn2",
-         "quant_ffn_hidden", "block_480p17", "block_480p81", "block_480p81_fp8", "block_480p81_fp8attn")
+         "quant_ffn_hidden", "block_480p17", "block_480p81", "block_480p81_fp8", "block_480p81_fp8attn",
+         "packed_attn", "packed_rope", "packed_add_norm", "packed_gemm_lora")
 
 
 def bf(*shape):
@@ -119,6 +120,29 @@ def make_case(name: str, B: int):
         n = 16 * 21 * 60 * 104 if name == "euler" else 1 << 26
         x, vc, vu = (torch.randn(n, device="cuda") for _ in range(3))
         return (lambda: wd.wd_euler_cfg_step(x, vc, vu, 5.0, 1 / 12)), 16.0 * n, "B", B
+    cu = torch.arange(0, rows + 1, L, device="cuda", dtype=torch.int32)   # B requests of L rows
+    if name == "packed_attn":
+        q, k, v, o = (bf(rows, D) for _ in range(4))
+        return (lambda: wd.wd_attention_packed(wd.WD_BF16, H, H, 128, q, k, v, cu, cu, 128 ** -0.5, o)), \
+            4.0 * B * L * L * D, "FLOP", B
+    if name == "packed_rope":
+        q, k, g = bf(rows, D), bf(rows, D), torch.ones(D, device="cuda")
+        t = torch.arange(rows, device="cuda") % L
+        pos = torch.stack((t // 1560, t // 52 % 30, t % 52), 1).int()
+        axes, qo, ko = wd.wd_rope_axes.of((44, 42, 42)), torch.empty_like(q), torch.empty_like(k)
+        return (lambda: wd.wd_qknorm_rope_axes(wd.WD_BF16, 128, axes, pos, q, g, qo, k, g, ko)), 8.0 * rows * D, "B", B
+    if name == "packed_add_norm":
+        x, y, g = torch.randn(rows, D, device="cuda"), bf(rows, D), torch.ones(D, device="cuda")
+        s, q8, sc = torch.empty_like(x), torch.empty((rows, D), dtype=torch.uint8, device="cuda"), torch.empty(rows, device="cuda")
+        return (lambda: wd.wd_add_norm(wd.WD_F32, x, wd.WD_BF16, y, wd.WD_NORM_RMS, g, None, 1e-6, s, wd.WD_E4M3, q8, sc)), \
+            11.0 * rows * D, "B", B
+    if name == "packed_gemm_lora":
+        N, r = 3 * D, 32
+        A, W, bias, out = bf(rows, D), bf(N, D) * 0.02, torch.zeros(N, device="cuda"), bf(rows, N)
+        lora = wd.wd_lora.of(cu, torch.arange(B, device="cuda", dtype=torch.int32), bf(B, r, D) * 0.02, bf(B, N, r) * 0.1)
+        ws = torch.empty(wd.wd_gemm_lora_bytes(rows, B, r), dtype=torch.uint8, device="cuda")
+        return (lambda: wd.wd_gemm_lora(rows, N, D, A, W, bias, lora, wd.EPI_STORE, out, ws)), \
+            2.0 * rows * (N * D + r * (N + D)), "FLOP", B
     raise SystemExit(f"unknown case {name}")
 
 
