@@ -549,15 +549,17 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 nm2 = make_float2(-ref, -ref), sc2 = make_float2(p.scale_log2, p.scale_log2);
         float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // 16 keys: two in eight exponentials on the FMA pipe (k_attn_tc.cu).  A key that is left out has
+        // P = 0 on either pipe: its value row may hold anything finite, and 2^-125 of 3e38 is 7.
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {   // 16 keys: two in eight exponentials on the FMA pipe (k_attn_tc.cu)
+        for (int c = 0; c < 8; ++c) {
           uint32_t pk[8];
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
             const float2 s2 = make_float2(__uint_as_float(a[c >> 1][(c & 1) * 16 + k]),
                                           __uint_as_float(a[c >> 1][(c & 1) * 16 + k + 1]));
             const float2 arg = BIAS ? fadd2(s2, nm2) : ffma2(s2, sc2, nm2);
-            const float2 e = (k & 7) == 6 ? tca::exp2_fma2(arg) : make_float2(tca::ex2(arg.x), tca::ex2(arg.y));
+            const float2 e = (k & 7) == 6 ? tca::exp2_fma2<true>(arg) : make_float2(tca::ex2(arg.x), tca::ex2(arg.y));
             rs[(k >> 1) & 3] = fadd2(rs[(k >> 1) & 3], e);
             pk[k >> 1] = C::HALF ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
           }

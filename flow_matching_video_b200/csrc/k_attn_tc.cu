@@ -168,8 +168,15 @@ __device__ __forceinline__ float exp2_fma(float x) {
 
 // The same on two lanes at once with the packed fp32 instructions (f32x2): each
 // lane's operations and roundings are those of exp2_fma, in fewer instructions.
+// ZERO: arguments too small for a normal float give (almost) nothing instead of 2^-125.
+// At the limit -126.9998 the polynomial is just above 1 (c0 + 2e-4 c1 = 1.00007), so the
+// exponent field becomes 0 and what is left, 8e-43, is zero in bf16 and in half; at -127
+// itself q < 1 would borrow into the sign.  Between the limit and -126 the result is a
+// subnormal within 2^-127 of 2^x.
+template <bool ZERO = false>
 __device__ __forceinline__ float2 exp2_fma2(float2 x) {
-  x = make_float2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  constexpr float LOW = ZERO ? -126.9998f : -125.f;
+  x = make_float2(fmaxf(x.x, LOW), fmaxf(x.y, LOW));
   const float2 magic = make_float2(12582912.f, 12582912.f);
   const float2 t = fadd2(x, magic);
   const float2 f = fsub2(x, fsub2(t, magic));
