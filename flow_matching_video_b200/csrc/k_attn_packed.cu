@@ -129,8 +129,9 @@ __device__ __forceinline__ int2 extent(const int* cu, int s, int rows) {
   const int lo = min(max(cu[s], 0), rows);
   return make_int2(lo, max(min(cu[s + 1], rows), lo));
 }
-// Bias in log2 units; finite values stay finite (they absorb any score either way).
-__device__ __forceinline__ float log2_units(float b) { return isinf(b) ? b : fminf(fmaxf(b * LOG2E, -1e30f), 1e30f); }
+// Bias in log2 units; finite values stay finite (they absorb any score either way), NaN stays
+// NaN (fmaxf would drop it).
+__device__ __forceinline__ float log2_units(float b) { return isfinite(b) ? fminf(fmaxf(b * LOG2E, -1e30f), 1e30f) : b; }
 
 // Pair `index` of the grid (whole warp): the sequences with the most key blocks come
 // first (within each group of 32), and the pairs of one sequence run head after head, so

@@ -459,7 +459,7 @@ wd_status wd_gemm_fp8(int M, int N, int K, const void* Aq, const float* sa, cons
  *   blocks are skipped); the value rows of such keys still have to be finite.
  *   Finite values beyond +-1e30 / log2(e) count as that.
  * - A row that sees no key (an empty key range, or all of them left out) gives
- *   zeros.  A row of NaN or +inf scores gives NaN.  Rows of q outside every
+ *   zeros.  A row of NaN or +inf scores (from q, k or bias) gives NaN.  Rows of q outside every
  *   sequence (behind the last one, say) are not computed, and o is left as it
  *   was there; rows of k and v outside a sequence never reach its output,
  *   whatever they hold.

@@ -1,5 +1,6 @@
 """The packed-batch operators where a value that must not count meets one that
-could make it count: left-out keys with the largest value rows.
+could make it count: left-out keys with the largest value rows, and a bias that is
+NaN.
 
 The bounds are those stated in test_packed_gpu.py.
 """
@@ -63,3 +64,24 @@ def test_far_smaller_scores_have_no_weight(wd, dh):
     wd.wd_check()
     want, ab = attention64(q, k[:100], v[:100], [0, 70], [0, 100], 1, 1, dh, 0.5)
     assert_within(out, want, 2.0 ** -8 * want.abs() + 2.0 ** -7 * ab + 1e-6)
+
+
+@pytest.mark.parametrize("dh,td", [(64, torch.bfloat16), (128, torch.float16)])
+@pytest.mark.parametrize("at", [0, 3, 6, 7, 8, 16])
+def test_nan_bias_gives_nan_rows(wd, dh, td, at):
+    """A NaN in the table: NaN in every row that reads it, and in no other row or head."""
+    g = gen(at)
+    n, R = 300, 8
+    q, k, v = (normal(g, (n, 2 * dh), td) for _ in range(3))
+    bias = normal(g, (2, 2 * R + 1))
+    clean, out = (torch.empty((n, 2 * dh), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    code, cu = wd.WD_F16 if td == torch.float16 else wd.WD_BF16, ints([0, n])
+    wd.wd_attention_packed(code, 2, 2, dh, q, k, v, cu, cu, dh ** -0.5, clean, bias=bias)
+    bias[1, at] = math.nan
+    wd.wd_attention_packed(code, 2, 2, dh, q, k, v, cu, cu, dh ** -0.5, out, bias=bias)
+    wd.wd_check()
+    d = (torch.arange(n)[None] - torch.arange(n)[:, None]).clamp(-R, R) + R
+    hit = (d == at).any(1).cuda()
+    assert hit.any()
+    assert torch.equal(out[:, :dh], clean[:, :dh]) and torch.equal(out[~hit], clean[~hit])
+    assert out[hit, dh:].isnan().all()
