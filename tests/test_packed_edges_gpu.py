@@ -1,15 +1,19 @@
 """The packed-batch operators where a value that must not count meets one that
-could make it count: left-out keys with the largest value rows, and a bias that is
-NaN.
+could make it count: left-out keys with the largest value rows, a bias that is
+NaN, and half-precision operands at half precision's own tolerance.
 
-The bounds are those stated in test_packed_gpu.py.
+Bounds, besides those stated in test_packed_gpu.py:
+- half probabilities: the reference m of a row's final exponentials is the score of
+  one of its keys, whose 2^0 = 1 is in the row sum l, so l >= 1.  A probability below
+  the smallest normal half is stored with an absolute error of at most 2^-25, so o
+  errs by at most keys * 2^-25 * max |v| on top of the relative terms.
 """
 import math
 
 import pytest
 import torch
 
-from test_packed_gpu import attention64, gen, ints, normal, assert_within
+from test_packed_gpu import HALF, U, attention64, gen, ints, norm64, normal, offsets, rope64, assert_within
 
 pytestmark = pytest.mark.gpu
 HUGE = 3.3e38          # finite in bf16 and fp32
@@ -85,3 +89,48 @@ def test_nan_bias_gives_nan_rows(wd, dh, td, at):
     assert hit.any()
     assert torch.equal(out[:, :dh], clean[:, :dh]) and torch.equal(out[~hit], clean[~hit])
     assert out[hit, dh:].isnan().all()
+
+
+# ------------------------------------------------------------------ attention: half operands at half's tolerance
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("lq,lk", [([700], [700]), ([1, 300, 5], [1000, 129, 2000]), ([256, 40], [4000, 1])])
+@pytest.mark.parametrize("radius", [0, 100])
+def test_attention_packed_half_precision(wd, dh, lq, lk, radius):
+    g = gen(sum(lk) + dh + radius)
+    cu_q, cu_k = offsets(lq), offsets(lk)
+    q, k, v = normal(g, (cu_q[-1], 3 * dh), torch.float16), normal(g, (cu_k[-1], 3 * dh), torch.float16), normal(g, (cu_k[-1], 3 * dh), torch.float16)
+    bias = normal(g, (3, 2 * radius + 1), std=2.0) if radius else None
+    out = torch.empty((cu_q[-1], 3 * dh), dtype=torch.bfloat16, device="cuda")
+    wd.wd_attention_packed(wd.WD_F16, 3, 3, dh, q, k, v, ints(cu_q), ints(cu_k), dh ** -0.5, out, bias=bias)
+    wd.wd_check()
+    want, ab = attention64(q, k, v, cu_q, cu_k, 3, 3, dh, dh ** -0.5, bias)
+    for a, b, ka, kb in zip(cu_q, cu_q[1:], cu_k, cu_k[1:]):
+        sub = (kb - ka) * 2.0 ** -25 * float(v[ka:kb].float().abs().max())
+        assert_within(out[a:b], want[a:b], 2.0 ** -8 * want[a:b].abs() + 2 * 2.0 ** -11 * ab[a:b] + sub + 1e-6)
+
+
+# ------------------------------------------------------------------ row operators: widths of one or two chunks on several warps
+@pytest.mark.parametrize("D", [1280, 1792, 2560, 3584, 7168])
+@pytest.mark.parametrize("td", [torch.bfloat16, torch.float32], ids=str)
+def test_row_operators_at_more_widths(wd, D, td):
+    g = gen(D)
+    n, code = 19, wd.WD_F32 if td == torch.float32 else wd.WD_BF16
+    x, y = normal(g, (n, D), td), normal(g, (n, D), torch.bfloat16, 0.3)
+    gain, beta = 1 + normal(g, (D,), std=0.1), normal(g, (D,), std=0.1)
+    for rms in (True, False):
+        S, O = torch.empty_like(x), torch.empty((n, D), device="cuda")
+        wd.wd_add_norm(code, x, wd.WD_BF16, y, wd.WD_NORM_RMS if rms else wd.WD_NORM_LAYER, gain, beta, 1e-6, S, wd.WD_F32, O)
+        wd.wd_check()
+        s, want, bound = norm64(x, y, gain, beta, rms, 1e-6)
+        assert_within(S, s, (HALF[td] + U) * s.abs())
+        assert_within(O, want, bound + U * want.abs())
+    dh = 128
+    k = normal(g, (n, 256), td)
+    gk = 1 + normal(g, (256,), std=0.1)
+    pos = torch.randint(0, 1000, (n, 3), generator=g, device="cuda").int()
+    xo, ko = torch.empty_like(x), torch.empty_like(k)
+    wd.wd_qknorm_rope_axes(code, dh, wd.wd_rope_axes.of((44, 42, 42)), pos, x, gain, xo, k, gk, ko, 1e-6)
+    wd.wd_check()
+    for t, gn, out in ((x, gain, xo), (k, gk, ko)):
+        want, size = rope64(t, pos, gn, dh, (44, 42, 42), 10000.0, (1, 1, 1), 1e-6)
+        assert_within(out, want, 64 * U * size + HALF[td] * want.abs() + 2.0 ** -25)
