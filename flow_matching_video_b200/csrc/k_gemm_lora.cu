@@ -17,11 +17,12 @@
 // rows in some instantiations.)  Requests are in row order, so the meeting pairs (m, s)
 // form a monotone chain and m + s numbers the slabs without a table.
 //
-// T enters the second product in bf16, rounded once when the output has 2 bytes (its own
-// rounding is as large).  For fp32 outputs T is split in three bf16 parts, each the
-// remainder of those before, and all are multiplied: 2^-26 of the adapter's share is
-// lost instead of 2^-9; and the accumulators are summed in fp32 every few stages of K,
-// here across the cluster and in the dense part in registers (sum_every in k_gemm_tc.cu).
+// T enters the second product in bf16, rounded once when the output is bf16 (its own
+// rounding is as large).  For half outputs T is split in two bf16 parts, for fp32 ones in
+// three, each the remainder of those before, and all are multiplied: 2^-16 or 2^-24 of the
+// middle is lost at most, instead of 2^-8.  For fp32 outputs the accumulators are also summed
+// in fp32 every few stages of K, here across the cluster and in the dense part in registers
+// (sum_every in k_gemm_tc.cu).
 //
 // Measured (B200, a sustained loop): 43745 x 4608 x 1536 with rank 32 525 us, where wd_gemm
 // without adapters takes 515 - 530 (cold: 414 + 29 us for T, wd_gemm 425); 2500 x 1536 x 8960
@@ -598,7 +599,8 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   lora::Args a{};
   a.seg = l.seg; a.ids = l.adapter; a.scale = l.scale;
   a.n_seg = l.n_seg; a.n_adapters = l.n_adapters; a.rank = l.rank;
-  a.parts = (mode == EPI_F32 || mode == EPI_RESID) ? 3 : 1;
+  const bool fp32 = mode == EPI_F32 || mode == EPI_RESID;
+  a.parts = fp32 ? 3 : mode == EPI_STORE_F16 ? 2 : 1;
   a.M = M; a.N = N; a.K = K;
   const int BN = lora_tile(M, N);
   const bool pair = BN == LORA_PAIR;
@@ -623,7 +625,7 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
     const int k_iters = (K + lora::BK - 1) / lora::BK;
     const int64_t blocks = slabs * (a.tile / lora::BM);
     while (split < lora::MAX_SPLIT && blocks * split < sm_count() && k_iters >= 8 * split) split *= 2;
-    while (split < lora::MAX_SPLIT && a.parts > 1 && k_iters > 24 * split) split *= 2;
+    while (split < lora::MAX_SPLIT && fp32 && k_iters > 24 * split) split *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * split));
     cfg.blockDim = dim3(lora::THREADS);

@@ -543,10 +543,12 @@ size_t wd_gemm_lora_bytes(int M, int n_seg, int rank);
  * a the adapter of row m's request, then wd_gemm's epilogues (0, 1, 2, 3, 5) on v.
  * A [M, K], W [N, K] bf16 dense, N a multiple of 64, K a multiple of 8.  The
  * rank-wide middle A down^T is summed in fp32 and enters the second product
- * rounded to bf16 for 2-byte outputs, and as a sum of three bf16 parts (2^-26) for
- * fp32 outputs (epilogues 2 and 3), whose accumulation is rounded to nearest
- * every 512 of K instead of truncated throughout as in wd_gemm.  ws: wd_gemm_lora_bytes(M, n_seg, rank)
- * bytes, not shared with a call that may run at the same time.
+ * rounded to bf16 for bf16 outputs, as a sum of two bf16 parts (to 2^-16) for half
+ * outputs (epilogue 5) and of three (to 2^-24) for fp32 outputs (epilogues 2 and 3),
+ * whose accumulation is rounded to nearest every 512 of K instead of truncated
+ * throughout as in wd_gemm (a K of 512 or less is one such piece).  ws:
+ * wd_gemm_lora_bytes(M, n_seg, rank) bytes, not shared with a call that may run
+ * at the same time.
  * Errors: N, K, rank, n_seg (1 .. 65536), n_adapters < 1, M above 2^29,
  * n_adapters * max(N, rank) above 2^31 - 1 -> WD_ERR_SHAPE; the workspace -> WD_ERR_WORKSPACE. */
 wd_status wd_gemm_lora(int M, int N, int K, const void* A, const void* W, const float* bias, const wd_lora* lora,

@@ -1,19 +1,21 @@
 """The packed-batch operators where a value that must not count meets one that
 could make it count: left-out keys with the largest value rows, a bias that is
-NaN, and half-precision operands at half precision's own tolerance.
+NaN, and half-precision operands and outputs at half precision's own tolerance.
 
 Bounds, besides those stated in test_packed_gpu.py:
 - half probabilities: the reference m of a row's final exponentials is the score of
   one of its keys, whose 2^0 = 1 is in the row sum l, so l >= 1.  A probability below
   the smallest normal half is stored with an absolute error of at most 2^-25, so o
   errs by at most keys * 2^-25 * max |v| on top of the relative terms.
+- two bf16 parts of the rank-wide middle: the first leaves a remainder of at most
+  2^-8 of it, the second rounds that remainder by 2^-8: 2^-16.
 """
 import math
 
 import pytest
 import torch
 
-from test_packed_gpu import HALF, U, attention64, gen, ints, norm64, normal, offsets, rope64, assert_within
+from test_packed_gpu import HALF, U, attention64, gen, ints, lora64, norm64, normal, offsets, rope64, assert_within
 
 pytestmark = pytest.mark.gpu
 HUGE = 3.3e38          # finite in bf16 and fp32
@@ -134,3 +136,23 @@ def test_row_operators_at_more_widths(wd, D, td):
     for t, gn, out in ((x, gain, xo), (k, gk, ko)):
         want, size = rope64(t, pos, gn, dh, (44, 42, 42), 10000.0, (1, 1, 1), 1e-6)
         assert_within(out, want, 64 * U * size + HALF[td] * want.abs() + 2.0 ** -25)
+
+
+# ------------------------------------------------------------------ low-rank adapters
+@pytest.mark.parametrize("M,N,K,r", [(300, 64, 136, 16), (500, 256, 520, 72), (20000, 256, 264, 32)])
+def test_gemm_lora_half_output_keeps_half_precision(wd, M, N, K, r):
+    """Half outputs whose larger share comes from the adapter: its middle must not be
+    rounded more coarsely than the output."""
+    g = gen(M + r)
+    seg, ids = [0, 100, 107, M], [1, -1, 0]
+    A, W, bias = normal(g, (M, K), torch.bfloat16), normal(g, (N, K), torch.bfloat16, 0.002), normal(g, (N,), std=0.01)
+    down, up = normal(g, (2, r, K), torch.bfloat16, K ** -0.5), normal(g, (2, N, r), torch.bfloat16, 0.3)
+    out = torch.empty((M, N), dtype=torch.float16, device="cuda")
+    ws = torch.empty(wd.wd_gemm_lora_bytes(M, 3, r), dtype=torch.uint8, device="cuda").fill_(255)
+    wd.wd_gemm_lora(M, N, K, A, W, bias, wd.wd_lora.of(ints(seg), ints(ids), down, up), wd.EPI_STORE_F16, out, ws)
+    wd.wd_check()
+    want, err = lora64(A, W, bias, seg, ids, down, up, None, 3)      # its err holds 2^-24 of the middle
+    for a, b, i in zip(seg, seg[1:], ids):
+        if i >= 0:
+            err[a:b] += 2.0 ** -16 * (A[a:b].double() @ down[i].double().t()).abs() @ up[i].double().abs().t()
+    assert_within(out, want, (err + U * want.abs()) * (1 + 2.0 ** -11) + 2.0 ** -11 * want.abs() + 2.0 ** -25)
