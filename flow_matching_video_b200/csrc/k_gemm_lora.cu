@@ -12,10 +12,12 @@
 //
 // A row tile may hold the ends of several requests.  T is therefore stored in slabs, one
 // per (row tile m, request s) that meet, with the rows of other requests zero: the
-// extra K-blocks of a tile then add up to each row's own adapter.  (U has to be finite for
-// that.  Masking the rows in the MMA itself, by its vector of disabled lanes, gave wrong
-// rows in some instantiations.)  Requests are in row order, so the meeting pairs (m, s)
-// form a monotone chain and m + s numbers the slabs without a table.
+// extra K-blocks of a tile then add up to each row's own adapter.  A U that is not finite
+// breaks that (0 x inf): the epilogue of a tile that holds more than one request's rows
+// looks its accumulator through and sums what is not finite again (repair).  (Masking the
+// rows in the MMA itself, by its vector of disabled lanes, gave wrong rows in some
+// instantiations.)  Requests are in row order, so the meeting pairs (m, s) form a monotone
+// chain and m + s numbers the slabs without a table.
 //
 // T enters the second product in bf16, rounded once when the output is bf16 (its own
 // rounding is as large).  For half outputs T is split in two bf16 parts, for fp32 ones in
@@ -45,8 +47,9 @@ struct Args {
   int M, N, K;
   int m_tiles, tile;    // row tiles and their height: 128 rows, or 256 for SM pairs
   bf16* slabs;          // [m_tiles + n_seg][parts][tile][rank]
-  int4* tiles;          // [m_tiles]: where the tile's list begins, its length, and its first entry
+  int4* tiles;          // [m_tiles]: where the tile's list begins, its length (negative: mixed), and its first entry
   int2* list;           // [m_tiles + n_seg]: (slab, adapter) of each tile's active requests
+  const bf16 *A, *W, *up;
 };
 
 // Rows [x, y) of request s, kept inside the matrix whatever the offsets say.
@@ -78,19 +81,23 @@ __device__ __forceinline__ int last_where(int n, int lane, F&& ok) {
 }
 
 // The list of row tile m (a whole warp): from the first request that ends behind its
-// first row to the last that starts before its end, those that are active.
+// first row to the last that starts before its end, those that are active.  The tile is
+// mixed unless it has none or all its rows are of one.
 __device__ __forceinline__ void write_list(const Args& a, int m, int lane) {
   const int m0 = m * a.tile;
   const int first = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] <= m0; });
   const int last = last_where(a.n_seg, lane, [&](int s) { return a.seg[s] < m0 + a.tile; });
   const int begin = max(first, 0);
   int count = 0;
+  bool whole = false;
   int2 head = make_int2(0, 0);
   for (int s0 = begin; s0 <= last; s0 += 32) {
     const int s = s0 + lane;
     const int id = s <= last ? a.ids[s] : -1;
-    const bool act = s <= last && active(a, seg_rows(a, s), id, m0);
+    const int2 rows = s <= last ? seg_rows(a, s) : make_int2(0, 0);
+    const bool act = s <= last && active(a, rows, id, m0);
     const unsigned yes = __ballot_sync(0xffffffffu, act);
+    whole |= __any_sync(0xffffffffu, act && rows.x <= m0 && rows.y >= min(m0 + a.tile, a.M));
     if (act) a.list[m + begin + count + __popc(yes & ((1u << lane) - 1))] = make_int2(m + s, id);
     if (!count && yes) {
       const int src = __ffs(yes) - 1;
@@ -98,7 +105,77 @@ __device__ __forceinline__ void write_list(const Args& a, int m, int lane) {
     }
     count += __popc(yes);
   }
-  if (lane == 0) a.tiles[m] = make_int4(m + begin, count, head.x, head.y);
+  if (lane == 0) a.tiles[m] = make_int4(m + begin, whole ? count : -count, head.x, head.y);
+}
+
+// s[c] += sum over n (a multiple of 8) of x[i] y[c ld + i], in two fp32 sums, for eight rows c of y
+__device__ __forceinline__ void dot8(float2 (&s)[8], const bf16* x, const bf16* y, int64_t ld, int n) {
+#pragma unroll 2
+  for (int k = 0; k < n; k += 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(x + k);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 w = *reinterpret_cast<const uint4*>(y + c * ld + k);
+      s[c] = ffma2(unpack_bf16x2(u.x), unpack_bf16x2(w.x), s[c]);
+      s[c] = ffma2(unpack_bf16x2(u.y), unpack_bf16x2(w.y), s[c]);
+      s[c] = ffma2(unpack_bf16x2(u.z), unpack_bf16x2(w.z), s[c]);
+      s[c] = ffma2(unpack_bf16x2(u.w), unpack_bf16x2(w.w), s[c]);
+    }
+  }
+}
+
+// Whether all of a lane's N values are finite: four chains of three-way maxima, which keep a NaN.
+template <int N>
+__device__ __forceinline__ bool all_finite(const float (&v)[N]) {
+  float top[4] = {};
+#pragma unroll
+  for (int j = 0; j < N; j += 2)
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(top[j / 2 % 4]) : "f"(top[j / 2 % 4]), "f"(fabsf(v[j])), "f"(fabsf(v[j + 1])));
+  return top[0] < INFINITY && top[1] < INFINITY && top[2] < INFINITY && top[3] < INFINITY;
+}
+
+// One warp's 32 rows (TMEM lanes of tbase; this lane's is row m) and `cols` columns from n on of a mixed
+// tile's accumulator: each element that is not finite is summed again from the definition, over
+// the row's own adapter only (0 x inf of another request's U is never finite; a row whose own
+// numbers make it so stays so), eight columns at a time, since the lanes' rows of A come 16
+// bytes a line.  Not inlined: it runs when an adapter is broken (one wholly NaN: 891 x 1536 x 1536 0.8 ms, 2500 x
+// 1536 x 8960 in fp32 7 ms, 700 requests of one row at 4608 x 1536 1.9 ms).
+__device__ __noinline__ void repair(const Args& a, int4 row, int tile, uint32_t tbase, int cols, int m, int n) {
+  const bf16 *t = nullptr, *u = nullptr;   // the row's T and its adapter's U
+  for (int i = 0; i < -row.y; ++i) {
+    const int2 e = a.list[row.x + i];
+    const int2 rows = seg_rows(a, e.x - tile);
+    if (m >= rows.x && m < rows.y) {
+      t = a.slabs + (static_cast<int64_t>(e.x) * a.parts * a.tile + (m - tile * a.tile)) * a.rank;
+      u = a.up + static_cast<int64_t>(e.y) * a.N * a.rank;
+    }
+  }
+  for (int c = 0; c < cols; c += 8) {
+    uint32_t r[8];
+    tmem_ld8(tbase + c, r);
+    tmem_wait_ld();
+    uint32_t bad = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bad |= (r[j] & 0x7f800000u) == 0x7f800000u ? 1u << j : 0u;
+    if (m >= a.M) bad = 0;
+    if (!__any_sync(0xffffffffu, bad)) continue;
+    if (bad) {
+      float2 s[8] = {};
+      if (t)
+        for (int p = 0; p < a.parts; ++p)
+          dot8(s, t + static_cast<int64_t>(p) * a.tile * a.rank, u + static_cast<int64_t>(n + c) * a.rank, a.rank, a.rank);
+      bool open = false;   // an element that its own adapter leaves finite
+#pragma unroll
+      for (int j = 0; j < 8; ++j) open |= (bad >> j & 1u) && isfinite(s[j].x + s[j].y);
+      if (open) dot8(s, a.A + static_cast<int64_t>(m) * a.K, a.W + static_cast<int64_t>(n + c) * a.K, a.K, a.K);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (bad >> j & 1u) r[j] = __float_as_uint(s[j].x + s[j].y);
+    }
+    __syncwarp();
+    tmem_st8(tbase + c, r);
+  }
+  tmem_wait_st();
 }
 
 // The extra K-blocks of gemm_body: request after request, part after part.
@@ -124,7 +201,43 @@ struct Extra {
     return t;
   }
   __device__ __forceinline__ int per_part() const { return (a.rank + BK - 1) / BK; }
-  __device__ __forceinline__ int count(const Row& r) const { return r.y * a.parts * per_part(); }
+  __device__ __forceinline__ int count(const Row& r) const { return abs(r.y) * a.parts * per_part(); }
+  // An epilogue warp's share of a tile (COLS columns), before it is taken out of TMEM: repaired where a
+  // mixed tile has anything that is not finite.  Looking costs 0.3 - 0.5 us (14.5 -> 14.9 us at 891 x 1536 x
+  // 1536 of three requests, rank 16; 92 us of 5820 x 4608 x 1536 of 60 requests as before).
+  template <int COLS>
+  __device__ __forceinline__ void check(const Row& r, int tile, uint32_t tbase, int m, int n) const {
+    constexpr int STEP = COLS % 64 ? 32 : 64;
+    if (r.y >= 0) return;
+    bool ok = true;
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += STEP) {
+      uint32_t u[STEP / 32][32];
+#pragma unroll
+      for (int i = 0; i < STEP / 32; ++i) tmem_ld32(tbase + c + 32 * i, u[i]);
+      tmem_wait_ld();
+      float v[STEP];
+#pragma unroll
+      for (int j = 0; j < STEP; ++j) v[j] = __uint_as_float(u[j / 32][j % 32]);
+      ok &= all_finite(v);
+    }
+    if (__any_sync(0xffffffffu, !ok)) repair(a, r, tile, tbase, COLS, m, n);
+  }
+  // The same with the sums in registers: they go back to TMEM for the repair.
+  template <int COLS>
+  __device__ __forceinline__ void check(const Row& r, int tile, uint32_t tbase, float (&v)[COLS], int m, int n) const {
+    if (r.y >= 0 || __all_sync(0xffffffffu, all_finite(v))) return;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+      uint32_t u[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(v[c + j]);
+      tmem_st32(tbase + c, u);
+    }
+    tmem_wait_st();
+    repair(a, r, tile, tbase, COLS, m, n);
+    tcg::add_columns(tbase, v, true);
+  }
   // MMAs of the k-th extra block: 16 columns each, none for the zeros behind rank
   __device__ __forceinline__ int steps(int k) const {
     const int left = a.rank - k % per_part() * BK;
@@ -133,8 +246,9 @@ struct Extra {
   template <typename F>
   __device__ __forceinline__ void each(const Row& r, int n0, F&& load) const {
     int2 e = make_int2(r.z, r.w);
-    for (int i = 0; i < r.y; ++i) {
-      const int2 next = i + 1 < r.y ? a.list[r.x + i + 1] : e;   // fetched while this one's loads are issued
+    const int n = abs(r.y);
+    for (int i = 0; i < n; ++i) {
+      const int2 next = i + 1 < n ? a.list[r.x + i + 1] : e;   // fetched while this one's loads are issued
       for (int p = 0; p < a.parts; ++p)
         for (int k = 0; k < a.rank; k += BK)
           if (!load(tmT, k, (e.x * a.parts + p) * a.tile, tmU, k, e.y * a.N + n0)) return;
@@ -301,20 +415,26 @@ k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     };
     bool ok = true;
+    ex.wait();
     for (int t = first; t < tiles && ok; t += step) {
       const int m0 = t / n_tiles * 256 + rank * BM, n0 = t % n_tiles * BN2;
+      const Extra::Row row = ex.row(t / n_tiles);
       if constexpr (SUM > 0) {
         float v[COLS];
         for (int k = 0; k < k_iters && ok; k += SUM) {
           ok = wait();
           if (!ok) break;
-          tcg::add_columns(tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN2 + c_begin, v, k == 0);
+          const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN2 + c_begin;
+          tcg::add_columns(tbase, v, k == 0);
+          if (k + SUM >= k_iters) ex.check(row, t / n_tiles, tbase, v, m0 + q * 32 + lane, n0 + c_begin);
           release();
         }
         if (ok) tcg::epi_sums<MODE>(ep, tmX, stg + (warp - 2) * 1024, lane, v, m0 + q * 32, n0 + c_begin, a.M);
       } else {
         ok = wait();
         if (!ok) break;
+        ex.check<COLS>(row, t / n_tiles, tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN2 + c_begin,
+                       m0 + q * 32 + lane, n0 + c_begin);
         tcg::epi_tile<BN2, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN2, m0, n0, a.M, chunk);
         release();
       }
@@ -602,6 +722,7 @@ static wd_status gemm_lora(int M, int N, int K, const void* A, const void* W, co
   const bool fp32 = mode == EPI_F32 || mode == EPI_RESID;
   a.parts = fp32 ? 3 : mode == EPI_STORE_F16 ? 2 : 1;
   a.M = M; a.N = N; a.K = K;
+  a.A = static_cast<const bf16*>(A); a.W = static_cast<const bf16*>(W); a.up = static_cast<const bf16*>(l.up);
   const int BN = lora_tile(M, N);
   const bool pair = BN == LORA_PAIR;
   a.tile = pair ? 256 : 128;

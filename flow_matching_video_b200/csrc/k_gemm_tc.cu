@@ -446,15 +446,20 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     int acc = 0;
     uint32_t acc_phase = 0;
     uint32_t chunk = 0;   // staging tiles used so far (alternating)
+    [[maybe_unused]] typename X::Row row{};
+    if constexpr (X::ON) ex.wait();
     if constexpr (SUM > 0) {
       const int parts = (k_iters + SUM - 1) / SUM, q = warp & 3;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         float v[COLS];
+        if constexpr (X::ON) row = ex.row(t / n_tiles);
         for (int p = 0; p < parts; ++p) {
           if (!mbar_wait_warp(&tfull[acc], acc_phase, SITE_TFULL)) { ok = false; break; }
           tc_fence_after();
-          add_columns(tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + c_begin, v, p == 0);
+          const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + c_begin;
+          add_columns(tbase, v, p == 0);
+          if (p == parts - 1) ex.check(row, t / n_tiles, tbase, v, t / n_tiles * BM + q * 32 + lane, t % n_tiles * BN + c_begin);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&tempty[acc]);
@@ -465,8 +470,13 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     } else {
       for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int m0 = (t / n_tiles) * BM, n0 = (t % n_tiles) * BN;
+        if constexpr (X::ON) row = ex.row(t / n_tiles);
         if (!mbar_wait_warp(&tfull[acc], acc_phase, SITE_TFULL)) break;
         tc_fence_after();
+        if constexpr (X::ON)
+          ex.template check<COLS>(row, t / n_tiles,
+                                  tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + acc * BN + c_begin,
+                                  m0 + (warp & 3) * 32 + lane, n0 + c_begin);
         epi_tile<BN, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN, m0, n0, M, chunk);
         tc_fence_before();
         __syncwarp();

@@ -526,8 +526,9 @@ wd_status wd_add_norm(int64_t rows, int D, int x_dtype, const void* x, int y_dty
  * means none; several requests may share one).  Rows outside every request have
  * no adapter.  down [n_adapters, rank, K] and up [n_adapters, N, rank] bf16,
  * scale [n_adapters] fp32 or NULL (1).  rank a multiple of 8 in 8..256 (smaller
- * ranks are padded with zeros).  up has to be finite: requests may share a tile
- * of 128 rows, in which one's adapter is multiplied by zeros in the others' rows. */
+ * ranks are padded with zeros).  NaN or infinities in A, down, up or scale reach
+ * the rows of the requests they belong to and no others: the call takes longer
+ * where such an up meets other requests' rows in a tile of 128 or 256. */
 typedef struct {
   int n_seg, n_adapters, rank;
   const int *seg, *adapter;

@@ -1,6 +1,7 @@
 """The packed-batch operators where a value that must not count meets one that
 could make it count: left-out keys with the largest value rows, a bias that is
-NaN, and half-precision operands and outputs at half precision's own tolerance.
+NaN, adapters that are not finite next to requests that are, and half-precision
+operands and outputs at half precision's own tolerance.
 
 Bounds, besides those stated in test_packed_gpu.py:
 - half probabilities: the reference m of a row's final exponentials is the score of
@@ -9,6 +10,8 @@ Bounds, besides those stated in test_packed_gpu.py:
   errs by at most keys * 2^-25 * max |v| on top of the relative terms.
 - two bf16 parts of the rank-wide middle: the first leaves a remainder of at most
   2^-8 of it, the second rounds that remainder by 2^-8: 2^-16.
+- an element computed again by 8 fp32 sums errs by less than 2 K u sum|a b|, like
+  one of the tensor cores.
 """
 import math
 
@@ -156,3 +159,69 @@ def test_gemm_lora_half_output_keeps_half_precision(wd, M, N, K, r):
         if i >= 0:
             err[a:b] += 2.0 ** -16 * (A[a:b].double() @ down[i].double().t()).abs() @ up[i].double().abs().t()
     assert_within(out, want, (err + U * want.abs()) * (1 + 2.0 ** -11) + 2.0 ** -11 * want.abs() + 2.0 ** -25)
+
+
+def lora_with_bad_up(wd, lens, ids, M, N, K, r, epi, bad, start=0, seed=0):
+    """A run with adapter 2's `up` not finite at the places `bad` [(n, j, value)], against the
+    formula: finite elements within their bounds, and not finite exactly where the formula is not."""
+    g = gen(seed + M + N + K + r)
+    seg = offsets(lens, start)
+    A, W, bias = normal(g, (M, K), torch.bfloat16), normal(g, (N, K), torch.bfloat16, 0.05), normal(g, (N,), std=0.1)
+    down, up = normal(g, (3, r, K), torch.bfloat16, K ** -0.5), normal(g, (3, N, r), torch.bfloat16, 0.3)
+    scale = torch.rand(3, generator=g, device="cuda") + 0.5
+    for n, j, _ in bad:
+        up[2, n, j] = 0
+    fp32 = epi in (wd.EPI_F32, wd.EPI_RESID)
+    v, err = lora64(A, W, bias, seg, ids, down, up, scale, 3 if fp32 else 1)
+    hit = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    for a, b, i in zip(seg, seg[1:], ids):
+        if i == 2:
+            for n, _, _ in bad:
+                hit[a:b, n] = True
+    for n, j, x in bad:
+        up[2, n, j] = x
+    ga = normal(g, (N,)) + 3 if epi == wd.EPI_RESID else None
+    out = normal(g, (M, N)) if fp32 else torch.empty((M, N), dtype=torch.float16 if epi == wd.EPI_STORE_F16 else torch.bfloat16, device="cuda")
+    if epi == wd.EPI_RESID:
+        want = out.double() + ga.double() * v
+        bound = ga.double().abs() * err + 2 * U * (out.double().abs() + (ga.double() * v).abs())
+    elif epi == wd.EPI_GELU:
+        want = v * 0.5 * torch.erfc(-v / math.sqrt(2.0))
+        bound = 1.13 * err + 1e-6 * (want.abs() + 1)
+    else:
+        want, bound = v, err + U * v.abs()
+    if not fp32:
+        h = HALF[out.dtype]
+        bound = bound * (1 + h) + h * want.abs() + (2.0 ** -25 if out.dtype == torch.float16 else 0)
+    ws = torch.empty(wd.wd_gemm_lora_bytes(M, len(ids), r), dtype=torch.uint8, device="cuda").fill_(255)
+    wd.wd_gemm_lora(M, N, K, A, W, bias, wd.wd_lora.of(ints(seg), ints(ids), down, up, scale), epi, out, ws, gate_a=ga)
+    wd.wd_check()
+    finite = torch.isfinite(out)
+    assert not finite[hit].any(), "an element of the adapter's own rows is finite where the formula is not"
+    assert finite[~hit].all(), f"{int((~finite & ~hit).sum())} elements of other requests or columns are not finite"
+    assert_within(out.masked_fill(hit, 0.0), want.masked_fill(hit, 0.0), bound)
+
+
+BAD = [(0, 0, math.nan), (17, 3, math.inf), (63, 7, -math.inf), (40, 1, math.nan)]
+
+
+@pytest.mark.parametrize("epi", [0, 1, 2, 3, 5])
+@pytest.mark.parametrize("N,K,r", [(64, 136, 8), (128, 520, 40), (256, 1104, 72)])
+def test_gemm_lora_bad_up_stays_in_its_request(wd, epi, N, K, r):
+    """Requests and rows of none that share 128-row tiles with an adapter that is not finite."""
+    lora_with_bad_up(wd, [40, 1, 129, 0, 130, 3], [0, 2, 1, 2, 2, -1], 345, N, K, r, epi, BAD + [(N - 1, r - 1, math.inf)], start=9)
+
+
+@pytest.mark.parametrize("epi", [0, 1, 2, 3, 5])
+def test_gemm_lora_bad_up_stays_in_its_request_on_sm_pairs(wd, epi):
+    lens = [1, 127, 128, 200, 3, 0, 56, 600, 5000, 130, 126, 1, 9000]
+    lora_with_bad_up(wd, lens, [0, 1, 2, -1, 1, 0, 2, 0, 1, 2, 0, 1, 0], 20000, 256, 1104, 40, epi,
+                     BAD + [(130, 2, math.nan), (255, 39, -math.inf)], start=70)
+
+
+def test_gemm_lora_wholly_bad_up(wd):
+    """An adapter that is NaN throughout, one row in each of many tiles; and as the last tile's
+    only request, whose tile ends with the matrix."""
+    bad = [(n, j, math.nan) for n in range(64) for j in (0, 5)]
+    lora_with_bad_up(wd, [100, 1] * 12, [1, 2] * 12, 1300, 64, 264, 8, 0, bad)
+    lora_with_bad_up(wd, [128, 72], [0, 2], 200, 64, 264, 8, 2, bad)
