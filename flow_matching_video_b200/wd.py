@@ -78,13 +78,13 @@ class wd_lora(C.Structure):
         f = "wd_lora"
         na, r, k = _dims(down, 3, "down")
         n = _dims(up, 3, "up")[1]
-        ns = adapter.numel()
+        ns = _dims(adapter, 1, "adapter")[0]
         i32, bf16 = _torch_type(f, "i32"), _torch_types[WD_BF16]
         _take(f, i32, (ns + 1,), seg)
         _take(f, i32, (ns,), adapter)
         _take(f, bf16, (na, r, k), down)
         _take(f, bf16, (na, n, r), up)
-        _take(f, _torch_types[WD_F32], (na,), scale)
+        _take_given(f, _torch_types[WD_F32], (na,), scale)
         out = cls(ns, na, r, _p(seg), _p(adapter), _p(down), _p(up), _p(scale))
         out.tensors = (seg, adapter, down, up, scale)
         return out
@@ -168,21 +168,34 @@ def _ok(status: int, where: str):
 
 
 def _dims(t, n, name):
+    if t is None:
+        raise ValueError(f"{name}: a tensor is wanted, not None")
     if t.dim() != n:
         raise ValueError(f"{name}: {t.dim()} dimensions, not {n}")
     return t.shape
 
 
 def _take(where, dtype, shape, *tensors):
-    """Dense tensors (or None) of this element type and shape."""
+    """Dense tensors of this element type and shape."""
     for t in tensors:
-        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        if t is None:
+            raise ValueError(f"{where}: a dense {dtype} tensor {list(shape)} is wanted, not None")
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{where}: a dense {dtype} tensor {list(shape)} is wanted, not {t.dtype} {list(t.shape)}"
                              f" with strides {list(t.stride())}")
 
 
+def _take_given(where, dtype, shape, *tensors):
+    """The same for those that are given: None stands for no tensor."""
+    for t in tensors:
+        if t is not None:
+            _take(where, dtype, shape, t)
+
+
 def _rows(where, t, dtype, width, rows=None):
     """Row stride of a 2D tensor [rows, width] whose rows are dense."""
+    if t is None:
+        raise ValueError(f"{where}: {dtype} rows of {width} dense elements are wanted, not None")
     shape, strides = t.shape, t.stride()
     if t.dtype is not dtype or len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows) or \
             (strides[1] != 1 and width > 1):
@@ -377,7 +390,7 @@ def wd_attention_packed(dtype, heads, kv_heads, dh, q, k, v, cu_q, cu_k, scale, 
     o_rs = _rows(f, o, _torch_types[WD_BF16], wq, q.shape[0])
     if k_rs != v_rs:
         raise ValueError(f"{f}: row strides {k_rs} of k and {v_rs} of v")
-    n_seq = cu_q.numel() - 1
+    n_seq = _dims(cu_q, 1, "cu_q")[0] - 1
     _take(f, _torch_types["i32"], (n_seq + 1,), cu_q, cu_k)
     radius = 0
     if bias is not None:
@@ -405,8 +418,8 @@ def wd_qknorm_rope_axes(dtype, dh, axes: wd_rope_axes, pos, q, g_q, q_out, k=Non
     if (k is None) != (k_out is None) or dh <= 0 or wq % dh or wk % dh:
         raise ValueError(f"{f}: rows of {wq} and {wk} elements with heads of {dh}; k and k_out go together")
     _take(f, _torch_types["i32"], (rows, 3), pos)
-    _take(f, f32, (wq,), g_q)
-    _take(f, f32, (wk,), g_k)
+    _take_given(f, f32, (wq,), g_q)
+    _take_given(f, f32, (wk,), g_k)
     dev, (q_, qo_, p_, k_, ko_, gq_, gk_) = _pointers(f, q, q_out, pos, k, k_out, g_q, g_k)
     _launch(f, dev, stream, _lib.wd_qknorm_rope_axes, dtype, rows, dh, axes, p_, q_, q_rs, wq // dh, gq_, qo_, qo_rs, k_, k_rs,
             wk // dh, gk_, ko_, ko_rs, eps)
@@ -418,12 +431,13 @@ def wd_add_norm(x_dtype, x, y_dtype, y, norm, gain, beta, eps, sum, out_dtype, o
     f = "wd_add_norm"
     tx, f32 = _torch_type(f, x_dtype), _torch_types[WD_F32]
     shape = rows, D = _dims(x, 2, "x")
-    _take(f, tx, shape, x, sum)
+    _take(f, tx, shape, x)
+    _take_given(f, tx, shape, sum)
     if y is not None:
         _take(f, _torch_type(f, y_dtype), shape, y)
     _take(f, _torch_type(f, out_dtype), shape, out)
-    _take(f, f32, (D,), gain, beta)
-    _take(f, f32, (rows,), scale)
+    _take_given(f, f32, (D,), gain, beta)
+    _take_given(f, f32, (rows,), scale)
     dev, (x_, y_, g_, b_, s_, o_, sc_) = _pointers(f, x, y, gain, beta, sum, out, scale)
     _launch(f, dev, stream, _lib.wd_add_norm, rows, D, x_dtype, x_, y_dtype, y_, norm, g_, b_, eps, s_, out_dtype, o_, sc_)
 
@@ -441,7 +455,9 @@ def wd_gemm_lora(M, N, K, A, W, bias, lora: wd_lora, epilogue, out, ws, gate_a=N
     _take(f, bf16, (N, K), W)
     _take(f, f32 if epilogue in (EPI_F32, EPI_RESID) else _torch_types[WD_F16] if epilogue == EPI_STORE_F16 else bf16,
           (M, N), out)
-    _take(f, f32, (N,), bias, gate_a, gate_b)
+    _take_given(f, f32, (N,), bias, gate_a, gate_b)
+    if ws is None:
+        raise ValueError(f"{f}: a workspace is wanted, not None")
     if not hasattr(lora, "tensors"):
         raise ValueError(f"{f}: a wd_lora made by wd_lora.of is wanted (it holds the tensors)")
     down, up = lora.tensors[2:4]

@@ -108,3 +108,14 @@ def test_what_fits_is_refused_for_its_device_alone(wd, call):
 def test_what_does_not_fit_is_named(wd, call, kw, message):
     with pytest.raises(ValueError, match=message):
         CALLS[call](wd, **kw)
+
+
+@pytest.mark.parametrize("call,name", [
+    ("attention", "q"), ("attention", "k"), ("attention", "v"), ("attention", "o"), ("attention", "cu_q"), ("attention", "cu_k"),
+    ("rope", "pos"), ("rope", "q"), ("rope", "q_out"), ("norm", "x"), ("norm", "out"),
+    ("adapters", "seg"), ("adapters", "adapter"), ("adapters", "down"), ("adapters", "up"),
+    ("lora", "A"), ("lora", "W"), ("lora", "out"), ("lora", "ws"),
+])
+def test_a_missing_tensor_is_refused(wd, call, name):
+    with pytest.raises(ValueError, match="not None"):
+        CALLS[call](wd, **{name: None})
