@@ -456,8 +456,8 @@ def wd_gemm_lora(M, N, K, A, W, bias, lora: wd_lora, epilogue, out, ws, gate_a=N
     _take(f, f32 if epilogue in (EPI_F32, EPI_RESID) else _torch_types[WD_F16] if epilogue == EPI_STORE_F16 else bf16,
           (M, N), out)
     _take_given(f, f32, (N,), bias, gate_a, gate_b)
-    if ws is None:
-        raise ValueError(f"{f}: a workspace is wanted, not None")
+    if ws is None or not ws.is_contiguous():   # gaps of a view would be written like the rest
+        raise ValueError(f"{f}: a dense workspace is wanted, not {'None' if ws is None else f'one with strides {list(ws.stride())}'}")
     if not hasattr(lora, "tensors"):
         raise ValueError(f"{f}: a wd_lora made by wd_lora.of is wanted (it holds the tensors)")
     down, up = lora.tensors[2:4]

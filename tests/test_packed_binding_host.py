@@ -119,3 +119,9 @@ def test_what_does_not_fit_is_named(wd, call, kw, message):
 def test_a_missing_tensor_is_refused(wd, call, name):
     with pytest.raises(ValueError, match="not None"):
         CALLS[call](wd, **{name: None})
+
+
+def test_a_workspace_with_gaps_is_refused(wd):
+    """Its bytes are counted without the gaps, which belong to someone else."""
+    with pytest.raises(ValueError, match="a dense workspace is wanted, not one with strides"):
+        call_lora(wd, ws=torch.zeros((1024, 2048), dtype=torch.uint8)[:, :1024])
