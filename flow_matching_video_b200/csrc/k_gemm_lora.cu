@@ -144,7 +144,9 @@ __device__ __noinline__ void repair(const Args& a, int4 row, int tile, uint32_t 
   const bf16 *t = nullptr, *u = nullptr;   // the row's T and its adapter's U
   for (int i = 0; i < -row.y; ++i) {
     const int2 e = a.list[row.x + i];
-    const int2 rows = seg_rows(a, e.x - tile);
+    const int s = e.x - tile;   // offsets that decrease let tiles write into each other's lists
+    if (static_cast<unsigned>(s) >= static_cast<unsigned>(a.n_seg)) continue;
+    const int2 rows = seg_rows(a, s);
     if (m >= rows.x && m < rows.y) {
       t = a.slabs + (static_cast<int64_t>(e.x) * a.parts * a.tile + (m - tile * a.tile)) * a.rank;
       u = a.up + static_cast<int64_t>(e.y) * a.N * a.rank;

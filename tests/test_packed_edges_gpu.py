@@ -225,3 +225,27 @@ def test_gemm_lora_wholly_bad_up(wd):
     bad = [(n, j, math.nan) for n in range(64) for j in (0, 5)]
     lora_with_bad_up(wd, [100, 1] * 12, [1, 2] * 12, 1300, 64, 264, 8, 0, bad)
     lora_with_bad_up(wd, [128, 72], [0, 2], 200, 64, 264, 8, 2, bad)
+
+
+def test_gemm_lora_bad_offsets_stay_inside(wd):
+    """Offsets outside the matrix count as its ends.  Decreasing ones have unspecified results,
+    but stay inside the buffers, a broken adapter's repair too: rows behind M are left alone."""
+    g = gen(30)
+    M, N, K, r = 500, 128, 136, 16
+    A, W = normal(g, (M, K), torch.bfloat16), normal(g, (N, K), torch.bfloat16, 0.1)
+    down, up = normal(g, (2, r, K), torch.bfloat16, K ** -0.5), normal(g, (2, N, r), torch.bfloat16)
+    ids = [0, 1, 0, 1, 1, 0]
+    ws = torch.empty(wd.wd_gemm_lora_bytes(M, len(ids), r), dtype=torch.uint8, device="cuda").fill_(255)
+
+    def run(seg):
+        room = torch.full((M + 100, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        wd.wd_gemm_lora(M, N, K, A, W, None, wd.wd_lora.of(ints(seg), ints(ids), down, up), wd.EPI_STORE, room[:M], ws)
+        wd.wd_check()
+        assert (room[M:] == 7.0).all()
+        return room[:M]
+
+    want = run([0, 100, 230, 230, 300, 490, 500])
+    assert torch.equal(run([-(1 << 30), 100, 230, 230, 300, 490, 1 << 30]), want)
+    up[1, 5, 3] = math.nan
+    for seg in ([400, 300, 200, 100, 50, 20, 10], [0, 500, 0, 500, 0, 500, 0], [1 << 30, -5, 300, 2, 499, 128, 127], [500] * 7):
+        run(seg)
