@@ -475,7 +475,7 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       // that block's first key, counted from the warp's first row
       [[maybe_unused]] const int far = w.n_lo * BK - (w.l0 + t * BQ + quarter * 32);
       float m = -INFINITY, l = 0.f;
-      for (int n = 0; n < nb; ++n) {
+      for (int kb = 0; kb < nb; ++kb) {
         if (!mbar_wait_warp(&s_full[t], blocks & 1u, SITE_S)) { ok = false; break; }
         ++blocks;
         tc_fence_after();
@@ -485,7 +485,7 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         tmem_wait_ld();
         if constexpr (BIAS) {   // a = scale * s + bias, log2 units
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-          const int d = far + n * BK;
+          const int d = far + kb * BK;
           const bool past = d - 31 >= R, before = d + BK - 1 <= -R;   // warp-uniform
           if (past || before) {
             const float cb = tab[past ? 2 * (R + PAD) : 0];
@@ -511,7 +511,7 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
               }
           }
         }
-        const int valid = keys - n * BK;
+        const int valid = keys - kb * BK;
         if (valid < BK) {   // keys behind the sequence's end
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -533,7 +533,7 @@ k_attn_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const bool grow = !(mx <= m + tca::RESCALE_THRESHOLD);
         const float alpha = grow ? tca::ex2(m - mx) : 1.f;
         if (grow) m = mx;
-        if (__any_sync(0xffffffffu, grow) && n > 0) {
+        if (__any_sync(0xffffffffu, grow) && kb > 0) {
           // P V of the block before has completed: its commit precedes the S waited for
 #pragma unroll 1
           for (int c = 0; c < DH / 32; ++c) {
