@@ -110,7 +110,7 @@ __device__ __forceinline__ void write_list(const Args& a, int m, int lane) {
 
 // s[c] += sum over n (a multiple of 8) of x[i] y[c ld + i], in two fp32 sums, for eight rows c of y
 __device__ __forceinline__ void dot8(float2 (&s)[8], const bf16* x, const bf16* y, int64_t ld, int n) {
-#pragma unroll 2
+#pragma unroll 1   // 2: 168 registers instead of 135, which all launches pay for (0.2 us)
   for (int k = 0; k < n; k += 8) {
     const uint4 u = *reinterpret_cast<const uint4*>(x + k);
 #pragma unroll
@@ -138,8 +138,8 @@ __device__ __forceinline__ bool all_finite(const float (&v)[N]) {
 // tile's accumulator: each element that is not finite is summed again from the definition, over
 // the row's own adapter only (0 x inf of another request's U is never finite; a row whose own
 // numbers make it so stays so), eight columns at a time, since the lanes' rows of A come 16
-// bytes a line.  Not inlined: it runs when an adapter is broken (one wholly NaN: 891 x 1536 x 1536 0.8 ms, 2500 x
-// 1536 x 8960 in fp32 7 ms, 700 requests of one row at 4608 x 1536 1.9 ms).
+// bytes a line.  Not inlined: it runs when an adapter is broken (one wholly NaN: 891 x 1536 x 1536 1.0 ms, 2500 x
+// 1536 x 8960 in fp32 8 ms, 700 requests of one row at 4608 x 1536 2.1 ms).
 __device__ __noinline__ void repair(const Args& a, int4 row, int tile, uint32_t tbase, int cols, int m, int n) {
   const bf16 *t = nullptr, *u = nullptr;   // the row's T and its adapter's U
   for (int i = 0; i < -row.y; ++i) {
@@ -204,28 +204,35 @@ struct Extra {
   }
   __device__ __forceinline__ int per_part() const { return (a.rank + BK - 1) / BK; }
   __device__ __forceinline__ int count(const Row& r) const { return abs(r.y) * a.parts * per_part(); }
-  // An epilogue warp's share of a tile (COLS columns), before it is taken out of TMEM: repaired where a
-  // mixed tile has anything that is not finite.  Looking costs 0.3 - 0.5 us (14.5 -> 14.9 us at 891 x 1536 x
-  // 1536 of three requests, rank 16; 92 us of 5820 x 4608 x 1536 of 60 requests as before).
-  template <int COLS>
-  __device__ __forceinline__ void check(const Row& r, int tile, uint32_t tbase, int m, int n) const {
-    constexpr int STEP = COLS % 64 ? 32 : 64;
-    if (r.y >= 0) return;
-    bool ok = true;
+  // An epilogue warp's share of a tile (COLS columns of its lanes), taken out of TMEM by out().  In a mixed
+  // tile, if anything of it is not finite, it is repaired and taken out again, over what the first time
+  // stored.  Looking it through while those stores are under way takes 0.1 us in a graph (13.3 -> 13.4 at 891 x
+  // 1536 x 1536 of three requests, rank 16; 14.5 -> 14.9 us a call on a stream), before them 0.3 us more; larger
+  // batches take as long as without.  For epilogues that store; those that add to the output sum in
+  // registers and use check().
+  template <int COLS, typename F>
+  __device__ __forceinline__ void take_out(const Row& r, int tile, uint32_t tbase, int m, int n, F&& out) const {
+    for (bool last = r.y >= 0;; last = true) {
+      out();
+      if (last) return;
+      bool ok = true;
 #pragma unroll 1
-    for (int c = 0; c < COLS; c += STEP) {
-      uint32_t u[STEP / 32][32];
+      for (int c = 0; c < COLS; c += 32) {
+        uint32_t u[32];
+        tmem_ld32(tbase + c, u);
+        tmem_wait_ld();
+        float v[32];
 #pragma unroll
-      for (int i = 0; i < STEP / 32; ++i) tmem_ld32(tbase + c + 32 * i, u[i]);
-      tmem_wait_ld();
-      float v[STEP];
-#pragma unroll
-      for (int j = 0; j < STEP; ++j) v[j] = __uint_as_float(u[j / 32][j % 32]);
-      ok &= all_finite(v);
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+        ok &= all_finite(v);
+      }
+      if (__all_sync(0xffffffffu, ok)) return;
+      bulk_wait_group<0>();   // of the lane that stores: performed, not only read
+      __syncwarp();
+      repair(a, r, tile, tbase, COLS, m, n);
     }
-    if (__any_sync(0xffffffffu, !ok)) repair(a, r, tile, tbase, COLS, m, n);
   }
-  // The same with the sums in registers: they go back to TMEM for the repair.
+  // The same for sums in registers, before they are taken out: they go back to TMEM for the repair.
   template <int COLS>
   __device__ __forceinline__ void check(const Row& r, int tile, uint32_t tbase, float (&v)[COLS], int m, int n) const {
     if (r.y >= 0 || __all_sync(0xffffffffu, all_finite(v))) return;
@@ -435,9 +442,10 @@ k_gemm_lora2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
       } else {
         ok = wait();
         if (!ok) break;
-        ex.check<COLS>(row, t / n_tiles, tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN2 + c_begin,
-                       m0 + q * 32 + lane, n0 + c_begin);
-        tcg::epi_tile<BN2, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN2, m0, n0, a.M, chunk);
+        ex.take_out<COLS>(row, t / n_tiles, tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN2 + c_begin,
+                          m0 + q * 32 + lane, n0 + c_begin, [&]() {
+          tcg::epi_tile<BN2, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN2, m0, n0, a.M, chunk);
+        });
         release();
       }
     }

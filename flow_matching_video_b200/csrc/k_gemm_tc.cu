@@ -473,11 +473,13 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         if constexpr (X::ON) row = ex.row(t / n_tiles);
         if (!mbar_wait_warp(&tfull[acc], acc_phase, SITE_TFULL)) break;
         tc_fence_after();
+        auto out = [&]() { epi_tile<BN, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN, m0, n0, M, chunk); };
         if constexpr (X::ON)
-          ex.template check<COLS>(row, t / n_tiles,
-                                  tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + acc * BN + c_begin,
-                                  m0 + (warp & 3) * 32 + lane, n0 + c_begin);
-        epi_tile<BN, MODE>(ep, tmX, stg, warp, lane, c_begin, tmem + acc * BN, m0, n0, M, chunk);
+          ex.template take_out<COLS>(row, t / n_tiles,
+                                     tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + acc * BN + c_begin,
+                                     m0 + (warp & 3) * 32 + lane, n0 + c_begin, out);
+        else
+          out();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[acc]);
