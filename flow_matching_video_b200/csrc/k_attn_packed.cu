@@ -15,8 +15,9 @@
 //    already loading, so short key sequences (prompts: four key blocks a pair) do not
 //    wait for a block's start and end each time.
 //  - Warp 0 finds each pair's sequence and tile by a scan over cu_q, with the
-//    sequences of most key blocks first (in groups of 32), so that the last pairs to
-//    run are short; it publishes the pair to the other warps.
+//    sequences of most key blocks first within each group of 32 (in a batch of up to 32 the
+//    last pairs to run are short; further groups follow in their own order); it publishes the
+//    pair to the other warps.
 //  - A sequence's last key block runs into the next sequence's rows (the TMA clips
 //    at the end of the buffer only).  Its scores behind the end become -inf before
 //    anything reads them, and its V rows are overwritten with zeros in shared
@@ -29,9 +30,12 @@
 //
 // Bound: per 128-key block of a pair the softmax's instructions (about 700 a warp, two warps a
 // sub-partition) take as long as the MMAs of 128-wide heads, and longer than those of 64-wide ones;
-// in a sustained loop the power cap holds both down.  Measured (B200): 7800 + 32760 tokens x 12 heads of 128
-// 5.9 - 6.2 ms (1120 - 1180 TFLOP/s; k_attn_tc on the two sequences one after the other 6.2 - 6.4 ms), 7800 +
-// 3185 + 405 tokens 0.37 - 0.43 ms, 43746 rows to 512 / 77 / 9 / 0 keys 0.127 - 0.149 ms.
+// in a sustained loop the power cap holds both down.  Measured (B200, sustained loops): 7800 + 32760 tokens x
+// 12 heads of 128 6.1 - 6.3 ms (1105 - 1140 TFLOP/s; cold 6.1; k_attn_tc on the two sequences one after the
+// other 6.2 - 6.4 ms), 7800 + 3185 + 405 tokens 0.44 ms (cold 0.47), 43746 rows to 512 / 77 / 9 / 0 keys 0.15 ms.
+// From some hundred sequences on find_work is the bound, whose scan begins at the first one for every pair:
+// of 77 tokens, 24 x 64 heads of 64 take 68 us (6.6 us a pair and SM), 300 x 16 heads 0.29 ms (9), 1000 x 16 2.3
+// ms (21), 3000 x 16 18 ms (56); 65536 of one token and head 0.36 s (820).
 #include "wd_internal.cuh"
 
 namespace wd {
@@ -42,8 +46,9 @@ constexpr int MAX_RADIUS = 1024, PAD = 160;   // PAD >= 127 + 31 + 1: a tile's r
 constexpr float LOG2E = 1.4426950408889634f;
 // Warps: 0 loads, 1 issues MMAs, 2 and 3 only fill their warpgroup, 4-7 and 8-11 are the
 // softmax warps of the tiles.  The first warpgroup hands registers on to the softmax, whose thread
-// holds a row of 128 scores: 120 and 192 a thread took 6.0 - 6.1 ms for 32760 tokens x 12 heads, 56 and 224
-// 6.4 - 6.7 (the issuing thread then recomputes its descriptors), 136 and 184 6.4 - 6.6, 168 each 6.9.
+// holds a row of 128 scores: 120 and 192 a thread took 6.0 - 6.1 ms for 32760 tokens x 12 heads in a
+// sustained loop (cold 5.2 - 5.3), 56 and 224 6.4 - 6.7 (the issuing thread then recomputes its
+// descriptors), 136 and 184 6.4 - 6.6, 168 each 6.9.
 constexpr int THREADS = 384, REGS_FEW = 120, REGS_MANY = 192;
 static_assert(128 * (REGS_FEW + 2 * REGS_MANY) <= THREADS * 168, "registers of the block at launch");
 

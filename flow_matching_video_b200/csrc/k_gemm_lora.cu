@@ -26,11 +26,13 @@
 // in fp32 every few stages of K, here across the cluster and in the dense part in registers
 // (sum_every in k_gemm_tc.cu).
 //
-// Measured (B200, a sustained loop): 43745 x 4608 x 1536 with rank 32 525 us, where wd_gemm
-// without adapters takes 515 - 530 (cold: 414 + 29 us for T, wd_gemm 425); 2500 x 1536 x 8960
-// with rank 64 to fp32 86 - 88 us (wd_gemm 72 - 74); 891 x 1536 x 1536 with rank 16 13.5 us
-// (wd_gemm 14.9).  Bound by the power cap and an SM's 64 bytes a clock from L2 where there are
-// many rows, by the latencies of two dependent launches where there are few.
+// Measured (B200, sustained loops on several boxes): 43745 x 4608 x 1536 with rank 32 to bf16
+// 455 - 540 us, to half 500 - 555, where wd_gemm without adapters takes 505 - 545; 2500 x 1536 x 8960
+// with rank 64 to fp32 77 - 91 us (wd_gemm 61 - 70); 891 x 1536 x 1536 with rank 16 14.4 - 16.6 us, 13.4
+// in a graph (wd_gemm 13 - 15); 700 requests of one row over four adapters, 4608 x 1536 with rank 16,
+// 210 us (wd_gemm 15): every request adds a K-block to its tile.  Bound by the power cap
+// and an SM's 64 bytes a clock from L2 where there are many rows, by the latencies of two dependent
+// launches where there are few.
 #include "wd_internal.cuh"
 
 namespace wd {

@@ -374,7 +374,10 @@ __global__ void __launch_bounds__(THREADS) k_add_norm(const AddNormArgs a, int w
 
 // ------------------------------------------------------------------ host side
 // How rows of D elements are laid out: nv chunks a lane and wpr warps that hold the row
-// exactly, with the fewest warps, or else a power of two of warps that holds it.
+// exactly, with the fewest warps, or else a power of two of warps that holds it.  Exact layouts
+// of one or two chunks a lane are the slow ones (bf16, GB/s of add + norm / QK-norm + rotary, cold): one
+// chunk, 1280 2905 / 2246 and 1792 3758 / 2891; two, 2560 4581 / 3734 and 3584 5329 / 4285; three and
+// four, 1536 6280 / 4970, 2048 6522 / 5381, 4096 6443 / 5331, 5120 5798 / 5074, 7168 6355 / 4930.
 struct RowShape {
   int wpr, nv;
   bool exact;
